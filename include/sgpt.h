@@ -35,7 +35,8 @@
  *     a non-zero *dev_info returns without touching its outputs. Clear it with
  *     sgpt_info_clear, read it with sgpt_sync_status.
  *     dev_info values: 0 ok; k > 0 pivot k (1-based column of H) was not
- *     positive; SGPT_INFO_NONFINITE; SGPT_INFO_TIMEOUT; SGPT_INFO_BAD_MASK.
+ *     positive; SGPT_INFO_NONFINITE; SGPT_INFO_TIMEOUT; SGPT_INFO_BAD_MASK;
+ *     SGPT_INFO_BAD_LENGTHS.
  *   - Size limits: 32 <= d_in <= 32768 and d_in % 32 == 0; 1 <= d_out <=
  *     16777216; ldw >= d_in and ldw % 4 == 0; every pointer 16-byte aligned.
  */
@@ -67,6 +68,7 @@ typedef enum sgpt_status {
 #define SGPT_INFO_NONFINITE (-1)
 #define SGPT_INFO_TIMEOUT (-2)
 #define SGPT_INFO_BAD_MASK (-3)
+#define SGPT_INFO_BAD_LENGTHS (-4) /* sequence offsets that decrease or leave the packed rows: SGPT_ERR_INVALID_ARG */
 
 #define SGPT_PATTERN_UNSTRUCTURED 0
 #define SGPT_PATTERN_NM 1
@@ -347,6 +349,73 @@ sgpt_status sgpt_sparse24_linear(const uint16_t* values, const uint32_t* meta_ti
 /* Wb = W rounded to bf16 (to nearest even), rows x cols, W leading
  * dimension ldw; Wb dense [rows x cols]. */
 sgpt_status sgpt_to_bf16(const float* W, int rows, int cols, int ldw, uint16_t* Wb, int* dev_info, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The forward of a jointly sparsified and quantized layer in 8-bit integers
+ * (SparseGPT review, sections 十五 and 十七, combine the sweep with
+ * quantization; how the result is multiplied is this library's reading).
+ *
+ * Weights, once per matrix: codes [d_out x d_in] int8 of W on its rows' grid
+ * [d_out x 2] fp32 (scale, zero point; sgpt_quant_grid's, or the qgrid the
+ * sweep used): code = clip(rint(W / scale) + zero, 0, 2^qbits - 1) -
+ * 2^(qbits - 1), in fp32, ties to even; qbits 2..8. For a W that the sweep
+ * quantized with this grid the codes stand for W exactly, a pruned weight
+ * included; any other W is rounded to its nearest level. Non-finite W or a
+ * zero scale: SGPT_INFO_NONFINITE. */
+sgpt_status sgpt_quant_codes(const float* W, int d_out, int d_in, int ldw, const float* grid, int qbits,
+                             int8_t* codes, int* dev_info, void* stream);
+
+/* Tokens, per call: X [n x d] bf16 with leading dimension ldx (ldx % 8 == 0)
+ * to Xq [n x d] int8 (dense) with a scale per token,
+ *   scale[t] = max_k |X[t][k]| / 127,  Xq[t][k] = rint(127 X[t][k] / max),
+ * ties to even, and sums[t] = sum_k Xq[t][k]. The division is IEEE fp32; for
+ * bf16 X the codes are the exact ones. A row of zeros has scale 0. A row with
+ * a NaN or an infinity sets SGPT_INFO_NONFINITE (and gets codes 0, scale
+ * NaN). 0 <= n <= 2^30; n == 0 launches nothing. X, Xq and the outputs must
+ * not overlap. */
+sgpt_status sgpt_quant_tokens(const uint16_t* X, int64_t n, int d, int64_t ldx, int8_t* Xq, float* scale,
+                              int32_t* sums, int* dev_info, void* stream);
+
+/* The same for the gated input of an MLP's down projection: row t is
+ * silu(G[t]) * U[t], silu(g) = g / (1 + e^-g), formed in fp32 and quantized
+ * without rounding it to bf16 first. G and U [n x d] bf16 with leading
+ * dimensions ldg, ldu (multiples of 8): two halves of one buffer are fine. */
+sgpt_status sgpt_quant_tokens_silu(const uint16_t* G, const uint16_t* U, int64_t n, int d, int64_t ldg, int64_t ldu,
+                                   int8_t* Xq, float* scale, int32_t* sums, int* dev_info, void* stream);
+
+/* Y [n x d_out] = X W^T from the 8-bit forms:
+ *   Y[t][r] = scale[t] * grid[r].scale *
+ *             (sum_k Xq[t][k] codes[r][k] - (grid[r].zero - 2^(qbits-1)) sums[t]),
+ * the bracket exact in int32 (tcgen05.mma.kind::i8), then rounded to fp32,
+ * multiplied by the two scales in fp32 and, for y_bf16 != 0, rounded to bf16.
+ * |Xq| <= 127, sums as sgpt_quant_tokens gives them and zero an integer in
+ * [0, 2^qbits - 1] keep the bracket inside int32. Y dense, fp32 or bf16.
+ * 0 <= n <= 2^30; any d_out; n == 0 launches nothing. */
+sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* sums, int64_t n, const int8_t* codes,
+                           const float* grid, int qbits, int d_in, int d_out, void* Y, int y_bf16, int* dev_info,
+                           void* stream);
+
+/* Causal attention over packed prompts, the token mixing between a decoder
+ * block's q/k/v and o projections (the pages give nothing of it):
+ *   O[i][h] = sum_{j <= i} softmax_j(scale Q[i][h] . K[j][g]) V[j][g],
+ * j over the rows of i's own sequence, g = h / (heads / kv_heads).
+ *   Q, O [n_tok x heads x width], K, V [n_tok x kv_heads x width] bf16; the
+ *     heads of a row are consecutive, rows are ldq, ldk, ldv, ldo elements
+ *     apart (multiples of 8), so parts of one q/k/v buffer can be passed.
+ *   offsets [n_seq + 1] int32, device: sequence s has the rows
+ *     offsets[s] .. offsets[s+1]; it may be empty. Rows outside every
+ *     sequence are not written. Offsets that decrease or leave [0, n_tok] set
+ *     SGPT_INFO_BAD_LENGTHS (the output is then unspecified).
+ *   width 64 or 128 (else SGPT_ERR_UNSUPPORTED), heads a multiple of
+ *     kv_heads, scale > 0 (usually width^-1/2), 0 <= n_tok <= 2^30.
+ * Scores, softmax and sums in fp32; the softmax's weights enter the second
+ * product in bf16; O is rounded once. Values in masked places (later rows,
+ * other sequences, rows outside) never reach a row's result as long as the
+ * row's own sequence is finite; a result that is not finite sets
+ * SGPT_INFO_NONFINITE. O must not overlap Q, K or V. */
+sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
+                           int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
+                           int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream);
 
 #ifdef __cplusplus
 }

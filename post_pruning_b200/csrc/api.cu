@@ -60,6 +60,12 @@ sgpt_status check_ws(void* ws, size_t have, size_t need) {
   return SGPT_OK;
 }
 
+// Tokens or packed rows of the 8-bit forward and the attention: row indices
+// plus a tile stay inside an int.
+bool valid_rows(int64_t n) { return n >= 0 && n <= (int64_t(1) << 30); }
+// A bf16 row stride: rows start on 16-byte boundaries.
+bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <= (int64_t(1) << 31); }
+
 }  // namespace
 
 extern "C" {
@@ -112,6 +118,7 @@ sgpt_status sgpt_sync_status(const int* dev_info, void* stream) {
   if (h == SGPT_INFO_NONFINITE) return SGPT_ERR_NONFINITE;
   if (h == SGPT_INFO_TIMEOUT) return SGPT_ERR_TIMEOUT;
   if (h == SGPT_INFO_BAD_MASK) return SGPT_ERR_BAD_MASK;
+  if (h == SGPT_INFO_BAD_LENGTHS) return SGPT_ERR_INVALID_ARG;
   return SGPT_ERR_CUDA;
 }
 
@@ -323,6 +330,68 @@ sgpt_status sgpt_prune_layer(float* W, int d_out, int d_in, int ldw, const uint1
     return s;
   if (pack) s = sgpt_pack_nm(W, d_out, d_in, ldw, mask_bits, p->n, p->m, values, meta, dev_info, stream);
   return s;
+}
+
+sgpt_status sgpt_quant_codes(const float* W, int d_out, int d_in, int ldw, const float* grid, int qbits,
+                             int8_t* codes, int* dev_info, void* stream) {
+  if (!W || !grid || !codes || !dev_info || !aligned16(W) || !aligned16(grid) || !aligned16(codes))
+    return SGPT_ERR_INVALID_ARG;
+  if (!valid_din(d_in) || !valid_dout(d_out) || ldw < d_in || ldw % 4 || qbits < 2 || qbits > 8)
+    return SGPT_ERR_INVALID_ARG;
+  return from_cuda(launch_quant_codes(W, ldw, d_out, d_in, grid, qbits, codes, dev_info, as_stream(stream)));
+}
+
+sgpt_status sgpt_quant_tokens(const uint16_t* X, int64_t n, int d, int64_t ldx, int8_t* Xq, float* scale,
+                              int32_t* sums, int* dev_info, void* stream) {
+  if (!valid_rows(n) || !valid_din(d) || !valid_ld(ldx, d) || !dev_info) return SGPT_ERR_INVALID_ARG;
+  if (n == 0) return SGPT_OK;
+  if (!X || !Xq || !scale || !sums || !aligned16(X) || !aligned16(Xq) || !aligned16(scale) || !aligned16(sums))
+    return SGPT_ERR_INVALID_ARG;
+  return from_cuda(launch_quant_tokens(X, n, d, ldx, Xq, scale, sums, dev_info, as_stream(stream)));
+}
+
+sgpt_status sgpt_quant_tokens_silu(const uint16_t* G, const uint16_t* U, int64_t n, int d, int64_t ldg, int64_t ldu,
+                                   int8_t* Xq, float* scale, int32_t* sums, int* dev_info, void* stream) {
+  if (!valid_rows(n) || !valid_din(d) || !valid_ld(ldg, d) || !valid_ld(ldu, d) || !dev_info)
+    return SGPT_ERR_INVALID_ARG;
+  if (n == 0) return SGPT_OK;
+  if (!G || !U || !Xq || !scale || !sums || !aligned16(G) || !aligned16(U) || !aligned16(Xq) || !aligned16(scale) ||
+      !aligned16(sums))
+    return SGPT_ERR_INVALID_ARG;
+  return from_cuda(launch_quant_tokens_silu(G, U, n, d, ldg, ldu, Xq, scale, sums, dev_info, as_stream(stream)));
+}
+
+sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* sums, int64_t n, const int8_t* codes,
+                           const float* grid, int qbits, int d_in, int d_out, void* Y, int y_bf16, int* dev_info,
+                           void* stream) {
+  if (!valid_rows(n) || !valid_din(d_in) || !valid_dout(d_out) || qbits < 2 || qbits > 8 || !dev_info)
+    return SGPT_ERR_INVALID_ARG;
+  if (n == 0) return SGPT_OK;
+  if (!Xq || !scale || !sums || !codes || !grid || !Y) return SGPT_ERR_INVALID_ARG;
+  const void* ptrs[] = {Xq, scale, sums, codes, grid, Y};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return SGPT_ERR_INVALID_ARG;
+  return from_cuda(launch_linear_i8(Xq, scale, sums, n, codes, grid, qbits, d_in, d_out, Y, y_bf16 != 0, dev_info,
+                                    as_stream(stream)));
+}
+
+sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
+                           int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
+                           int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream) {
+  if (!valid_rows(n_tok) || n_seq < 0 || !dev_info || heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536)
+    return SGPT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || width < 1) return SGPT_ERR_INVALID_ARG;
+  if (width != 64 && width != 128) return SGPT_ERR_UNSUPPORTED;
+  const int64_t qcols = (int64_t)heads * width, kcols = (int64_t)kv_heads * width;
+  if (!valid_ld(ldq, qcols) || !valid_ld(ldo, qcols) || !valid_ld(ldk, kcols) || !valid_ld(ldv, kcols))
+    return SGPT_ERR_INVALID_ARG;
+  if (n_tok == 0 || n_seq == 0) return SGPT_OK;
+  if (!Q || !K || !V || !O || !offsets || !aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) ||
+      (reinterpret_cast<uintptr_t>(offsets) & 3u))
+    return SGPT_ERR_INVALID_ARG;
+  if (attention_ctas(n_tok, n_seq, heads, kv_heads) > (long long)INT32_MAX) return SGPT_ERR_UNSUPPORTED;
+  return from_cuda(launch_attention(Q, ldq, K, ldk, V, ldv, offsets, n_seq, n_tok, heads, kv_heads, width, scale, O,
+                                    ldo, dev_info, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -53,6 +53,26 @@ cudaError_t launch_tile_meta(const uint32_t* meta, int rows, int d, uint32_t* ti
 cudaError_t launch_sparse24_gemm(const uint16_t* values_bf16, const uint32_t* tiles, int rows, int d,
                                  const uint16_t* X, long long n, float* Y, int* info, cudaStream_t st);
 
+// quant.cu
+cudaError_t launch_quant_codes(const float* W, long long ldw, int rows, int d, const float* grid, int bits,
+                               int8_t* codes, int* info, cudaStream_t st);
+cudaError_t launch_quant_tokens(const uint16_t* X, long long n, int d, long long ldx, int8_t* Xq, float* scale,
+                                int32_t* sums, int* info, cudaStream_t st);
+cudaError_t launch_quant_tokens_silu(const uint16_t* G, const uint16_t* U, long long n, int d, long long ldg,
+                                     long long ldu, int8_t* Xq, float* scale, int32_t* sums, int* info,
+                                     cudaStream_t st);
+
+// linear_i8.cu
+cudaError_t launch_linear_i8(const int8_t* Xq, const float* xs, const int32_t* xsum, long long n, const int8_t* codes,
+                             const float* grid, int bits, int d, int rows, void* Y, bool y_bf16, int* info,
+                             cudaStream_t st);
+
+// attention.cu
+long long attention_ctas(long long n_tok, int n_seq, int heads, int kv_heads);
+cudaError_t launch_attention(const uint16_t* Q, long long ldq, const uint16_t* K, long long ldk, const uint16_t* V,
+                             long long ldv, const int32_t* cu, int n_seq, long long n_tok, int heads, int kv_heads,
+                             int D, float scale, uint16_t* O, long long ldo, int* info, cudaStream_t st);
+
 // hessian_tc.cu
 size_t hessian_ws_bytes(int d, long long n);
 cudaError_t launch_hessian_tc(float* H, const uint16_t* X, long long n, int d, void* ws, int* info,

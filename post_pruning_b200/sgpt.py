@@ -10,6 +10,7 @@ missing, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -35,9 +36,11 @@ EXPORTS = (
     "sgpt_pack_nm", "sgpt_pack_nm_meta_words", "sgpt_quant_grid", "sgpt_recon_error", "sgpt_prune_layer",
     "sgpt_mlp_block_workspace_bytes", "sgpt_prune_mlp_block", "sgpt_linear_bf16", "sgpt_to_bf16",
     "sgpt_sparse24_linear", "sgpt_sparse24_meta_tiles_bytes", "sgpt_sparse24_tile_meta",
+    "sgpt_quant_codes", "sgpt_quant_tokens", "sgpt_quant_tokens_silu", "sgpt_linear_i8", "sgpt_attention",
 )
 DRIVER_SEQUENTIAL = 0
 DRIVER_PARALLEL = 1
+_HERE_ALREADY = contextlib.nullcontext()
 
 
 class SgptError(RuntimeError):
@@ -136,6 +139,12 @@ def lib() -> ctypes.CDLL:
         "sgpt_sparse24_linear": (i32, [vp, vp, i32, i32, vp, i64, vp, vp, vp]),
         "sgpt_sparse24_meta_tiles_bytes": (sz, [i32, i32]),
         "sgpt_sparse24_tile_meta": (i32, [vp, i32, i32, vp, vp]),
+        "sgpt_quant_codes": (i32, [vp, i32, i32, i32, vp, i32, vp, vp, vp]),
+        "sgpt_quant_tokens": (i32, [vp, i64, i32, i64, vp, vp, vp, vp, vp]),
+        "sgpt_quant_tokens_silu": (i32, [vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, vp]),
+        "sgpt_linear_i8": (i32, [vp, vp, vp, i64, vp, vp, i32, i32, i32, vp, i32, vp, vp]),
+        "sgpt_attention": (i32, [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, ctypes.c_float, vp, i64,
+                                 vp, vp]),
         "sgpt_recon_error": (i32, [vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]),
         "sgpt_prune_layer": (i32, [vp, i32, i32, i32, vp, i64, vp, vp, pp, vp, vp, vp, vp,
                                    vp, sz, vp, vp]),
@@ -166,11 +175,27 @@ def _dev(t: torch.Tensor, dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _on(*tensors: torch.Tensor):
+    """The device of `tensors`, which must be one, made current for a launch."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    return _HERE_ALREADY if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _rowmajor(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D tensor with unit column stride."""
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
     return t.stride(0)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """_rowmajor, where the stride of a single row (which no access uses) does
+    not matter."""
+    ld = _rowmajor(t, name)
+    return ld if t.shape[0] > 1 else t.shape[1]
 
 
 def _check(status: int, where: str):
@@ -391,6 +416,114 @@ def sparse24_linear(values: torch.Tensor, meta_tiles: torch.Tensor, X: torch.Ten
         raise ValueError("all operands must be contiguous")
     _check(lib().sgpt_sparse24_linear(_ptr(values), _ptr(meta_tiles), d_out, d_in, _ptr(X), n, _ptr(Y),
                                       _ptr(dev_info), _stream(stream)), "sgpt_sparse24_linear")
+
+
+def quant_codes(W: torch.Tensor, grid: torch.Tensor, codes: torch.Tensor, dev_info: torch.Tensor, qbits: int = 8,
+                stream=None):
+    """8-bit codes of W on its rows' grid (sgpt_quant_codes), once per weight
+    matrix: W [d_out, d_in] fp32, grid [d_out, 2] fp32 (quant_grid's, or the
+    qgrid of the sweep), codes [d_out, d_in] int8."""
+    _dev(W, torch.float32, "W")
+    _dev(grid, torch.float32, "grid")
+    _dev(codes, torch.int8, "codes")
+    ldw = _rowmajor(W, "W")
+    r, d = W.shape
+    if grid.shape != (r, 2) or codes.shape != (r, d) or not grid.is_contiguous() or not codes.is_contiguous():
+        raise ValueError("grid must be contiguous [d_out, 2] and codes contiguous [d_out, d_in]")
+    with _on(W, grid, codes, dev_info):
+        _check(lib().sgpt_quant_codes(_ptr(W), r, d, ldw, _ptr(grid), qbits, _ptr(codes), _ptr(dev_info),
+                                      _stream(stream)), "sgpt_quant_codes")
+
+
+def _token_outputs(n: int, d: int, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor):
+    _dev(Xq, torch.int8, "Xq")
+    _dev(scale, torch.float32, "scale")
+    _dev(sums, torch.int32, "sums")
+    if Xq.shape != (n, d) or scale.shape != (n,) or sums.shape != (n,):
+        raise ValueError("Xq must be [n, d], scale and sums [n]")
+    if not (Xq.is_contiguous() and scale.is_contiguous() and sums.is_contiguous()):
+        raise ValueError("Xq, scale and sums must be contiguous")
+
+
+def quant_tokens(X: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor,
+                 dev_info: torch.Tensor, stream=None):
+    """X [n, d] bf16 to 8 bits with a scale per token (sgpt_quant_tokens):
+    Xq [n, d] int8, scale [n] fp32, sums [n] int32 (the codes' row sums)."""
+    _dev(X, torch.bfloat16, "X")
+    ldx = _row_stride(X, "X")
+    n, d = X.shape
+    _token_outputs(n, d, Xq, scale, sums)
+    with _on(X, Xq, scale, sums, dev_info):
+        _check(lib().sgpt_quant_tokens(_ptr(X), n, d, ldx, _ptr(Xq), _ptr(scale), _ptr(sums), _ptr(dev_info),
+                                       _stream(stream)), "sgpt_quant_tokens")
+
+
+def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor,
+                      dev_info: torch.Tensor, stream=None):
+    """quant_tokens of silu(G) * U, an MLP's gated activation, without
+    rounding it to bf16 in between (sgpt_quant_tokens_silu)."""
+    _dev(G, torch.bfloat16, "G")
+    _dev(U, torch.bfloat16, "U")
+    ldg, ldu = _row_stride(G, "G"), _row_stride(U, "U")
+    n, d = G.shape
+    if U.shape != (n, d):
+        raise ValueError("G and U must have the same shape")
+    _token_outputs(n, d, Xq, scale, sums)
+    with _on(G, U, Xq, scale, sums, dev_info):
+        _check(lib().sgpt_quant_tokens_silu(_ptr(G), _ptr(U), n, d, ldg, ldu, _ptr(Xq), _ptr(scale),
+                                            _ptr(sums), _ptr(dev_info), _stream(stream)), "sgpt_quant_tokens_silu")
+
+
+def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: torch.Tensor, grid: torch.Tensor,
+              Y: torch.Tensor, dev_info: torch.Tensor, qbits: int = 8, stream=None):
+    """Y = X W^T in 8-bit integers (sgpt_linear_i8): Xq, scale, sums from
+    quant_tokens, codes [d_out, d_in] int8 from quant_codes with its grid and
+    qbits, Y [n, d_out] fp32 or bf16."""
+    _dev(codes, torch.int8, "codes")
+    _dev(grid, torch.float32, "grid")
+    if Xq.dim() != 2 or codes.dim() != 2:
+        raise ValueError("Xq must be [n, d_in] and codes [d_out, d_in]")
+    n, d_in = Xq.shape
+    d_out = codes.shape[0]
+    _token_outputs(n, d_in, Xq, scale, sums)
+    y_bf16 = Y.dtype == torch.bfloat16
+    _dev(Y, torch.bfloat16 if y_bf16 else torch.float32, "Y")
+    if codes.shape[1] != d_in or grid.shape != (d_out, 2) or Y.shape != (n, d_out):
+        raise ValueError("codes must be [d_out, d_in], grid [d_out, 2] and Y [n, d_out]")
+    if not (codes.is_contiguous() and grid.is_contiguous() and Y.is_contiguous()):
+        raise ValueError("codes, grid and Y must be contiguous")
+    with _on(Xq, scale, sums, codes, grid, Y, dev_info):
+        _check(lib().sgpt_linear_i8(_ptr(Xq), _ptr(scale), _ptr(sums), n, _ptr(codes), _ptr(grid), qbits, d_in, d_out,
+                                    _ptr(Y), y_bf16, _ptr(dev_info), _stream(stream)), "sgpt_linear_i8")
+
+
+def _heads(t: torch.Tensor, name: str) -> int:
+    """Row stride of [rows, heads, width] with consecutive heads."""
+    _dev(t, torch.bfloat16, name)
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [rows, heads, width] with consecutive heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.Tensor, O: torch.Tensor,
+              dev_info: torch.Tensor, scale: float | None = None, stream=None):
+    """Causal attention over packed prompts (sgpt_attention): Q, O [n_tok,
+    heads, width], K, V [n_tok, kv_heads, width] bf16 (width 64 or 128; rows
+    may be strided, e.g. parts of one q/k/v buffer), offsets [n_seq + 1] int32
+    on the device: sequence s has the rows offsets[s]:offsets[s + 1]. scale:
+    width ** -0.5 when None."""
+    ldq, ldk, ldv, ldo = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V"), _heads(O, "O")
+    _dev(offsets, torch.int32, "offsets")
+    n, heads, width = Q.shape
+    kv_heads = K.shape[1]
+    if K.shape != (n, kv_heads, width) or V.shape != K.shape or O.shape != Q.shape:
+        raise ValueError("Q and O must be [n_tok, heads, width], K and V [n_tok, kv_heads, width]")
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous [n_seq + 1]")
+    with _on(Q, K, V, O, offsets, dev_info):
+        _check(lib().sgpt_attention(_ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, _ptr(offsets), offsets.shape[0] - 1, n,
+                                    heads, kv_heads, width, width ** -0.5 if scale is None else scale, _ptr(O), ldo,
+                                    _ptr(dev_info), _stream(stream)), "sgpt_attention")
 
 
 def mlp_block_workspace(hidden: int, inter: int, n_tok: int, device="cuda") -> torch.Tensor:
