@@ -13,12 +13,23 @@
 // registers and a warp writes 32 consecutive channels of a token; and one
 // token costs a product of N = 16, not a row tile of 128.
 //
-// Persistent, one CTA per SM, warp-specialized: warp 0 feeds a ring of
-// 128-byte K stages by TMA (128-byte swizzle, out of range reads give zero
-// codes), warp 1 issues four MMAs (K = 32) per stage into one of two
-// accumulators, warps 2-5 drain the other. Tiles are walked in groups of 16
-// tile rows (rows fastest) so that resident CTAs share panels in L2. Every
-// wait is bounded as everywhere in this library.
+// Two kernels, both warp-specialized: warp 0 feeds a ring of 128-byte K
+// stages by TMA (128-byte swizzle, out of range reads give zero codes), warp 1
+// issues four MMAs (K = 32) per stage, warps 2-5 are the epilogue. Every wait
+// is bounded as everywhere in this library.
+//
+// linear_i8_pair_kernel, many tiles: persistent CTA pairs (cta_group::2) on
+// tiles of 256 channels x 256 tokens, each CTA with half of the rows of both
+// operands, two accumulators so that one is drained under the other's MMAs.
+// A single CTA on 128 x 256 tiles is bound by shared memory (48 KB written and
+// 48 KB read per 512 cycles of MMA, above its 128 bytes per cycle); the pair
+// needs 32 + 32 KB. Tiles are walked in groups of 8 tile rows (rows fastest)
+// so that resident pairs share panels in L2.
+//
+// linear_i8_split_kernel, few tiles: one tile of 128 channels x 16..128 tokens
+// per cluster, whose CTAs split K and add their int32 accumulators through
+// distributed shared memory. Bound by reading the codes: enough CTAs for all
+// SMs to read at once whatever the layer's width.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,53 +44,87 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kBM = 128, kBK = 128;             // output channels per tile; codes (bytes) of K per stage
+constexpr int kBM = 128, kBK = 128;             // output channels per CTA; codes (bytes) of K per stage
 constexpr int kThreads = 192;                   // producer, MMA, 4 epilogue warps
-constexpr int kGroupRows = 16;
 constexpr int kABytes = kBM * kBK;
-
-__host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * kBK; }
-__host__ __device__ constexpr int stages_for(int bn) { return bn > 128 ? 4 : bn > 64 ? 6 : 8; }
-__host__ __device__ constexpr size_t smem_for(int bn) {
-  return (size_t)stages_for(bn) * stage_bytes(bn) + 1024 + 256 + 2 * 8 * bn;
-}
-// accumulator columns: two of max(bn, 16), allocated as a power of two >= 32
-__host__ __device__ constexpr uint32_t tmem_cols(int bn) { return bn <= 16 ? 32u : 2u * bn; }
+constexpr long long kGraceCycles = 20000000ll;  // a failed pair's copies land within this (about 10 ms)
 
 // D int32, A and B signed bytes, both K-major.
-__host__ __device__ constexpr uint32_t idesc(int bn) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+template <int PAIR>
 __device__ __forceinline__ void mma_i8(uint32_t acc, uint64_t ad, uint64_t bd, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(acc),
-      "l"(ad), "l"(bd), "r"(id), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(acc),
+        "l"(ad), "l"(bd), "r"(id), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(acc),
+        "l"(ad), "l"(bd), "r"(id), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ void store_y(float* y, float v) { *y = v; }
 __device__ __forceinline__ void store_y(uint16_t* y, float v) { *y = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-template <int BN, class T>
-__global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
-    const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, int rows, int d, int n,
-    const float* __restrict__ grid, int half, const float* __restrict__ xs, const int32_t* __restrict__ xsum,
-    T* __restrict__ Y, int* info, const long long wait_cycles) {
-  constexpr int kStages = stages_for(BN), kStage = stage_bytes(BN);
+// What the epilogues need beside the accumulators.
+struct Out {
+  const float* grid;         // [rows][2] scale, zero point
+  const float* xs;           // [n] token scales
+  const int32_t* xsum;       // [n] token code sums
+  void* Y;                   // [n][rows]
+  int rows, n, half;
+};
+
+struct Channel {             // one output channel's scale and shifted zero point
+  float scale;
+  int zero;
+};
+__device__ __forceinline__ Channel channel(const Out& o, int row) {
+  Channel c{0.f, 0};
+  if (row < o.rows) {
+    const float2 g = *reinterpret_cast<const float2*>(o.grid + 2 * (long long)row);
+    c.scale = g.x;
+    c.zero = (int)g.y - o.half;
+  }
+  return c;
+}
+
+// ------------------------------------------------------------------ CTA pairs
+
+constexpr int kPairN = 256;                     // tokens per tile
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * kABytes;         // per CTA: 128 channels and 128 tokens
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + 1024 + 256 + 2 * 8 * kPairN;
+constexpr int kGroupRows = 8;                   // 256-channel tile rows walked together
+
+template <class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(
+    const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, int d, const Out out, int* info,
+    const long long wait_cycles) {
+  constexpr int kStages = kPairStages, kStage = kPairStage, BN = kPairN;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // both CTAs lay their shared memory out alike: the pair's barriers and
+  // operands are addressed by the same offsets
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
   float* tok_scale = reinterpret_cast<float*>(smem + kStages * kStage + 256);       // [2][BN]
   int32_t* tok_sum = reinterpret_cast<int32_t*>(tok_scale + 2 * BN);                // [2][BN]
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed;
-  if (cta_info_set(info)) return;
+  __shared__ int failed, skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt_count = cdiv(rows, kBM), nt_count = cdiv(n, BN), kt_count = cdiv(d, kBK);
+  const uint32_t rank = cluster_rank();
+  const int rows = out.rows, n = out.n;
+  const int mt_count = cdiv(rows, 2 * kBM), nt_count = cdiv(n, BN), kt_count = cdiv(d, kBK);
   const long long items = (long long)mt_count * nt_count;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t s0 = smem_u32(smem);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, mdone = tempty0 + 16;
@@ -87,22 +132,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
     prefetch_map(&wmap);
     prefetch_map(&xmap);
     failed = 0;
+    skip = info_set(info);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, 1);              // used in the first CTA
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 4);
+      mbar_init(tempty0 + 8 * b, 8);            // used in the first CTA: four warps of each
     }
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
-  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), tmem_cols(BN));
+  if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
   fence_before();
-  __syncthreads();
+  cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  // one decision for the pair: the first CTA's look at *info
+  const bool run = ld_cluster(map_rank(smem_u32(&skip), 0)) == 0;
 
   auto decode = [&](long long w, int& mt, int& nt) {
     const long long per_group = (long long)kGroupRows * nt_count;
@@ -115,9 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (lane == 0 && run) {
+      const uint32_t leader_full0 = map_rank(full0, 0);
       long long g = 0;
-      for (long long w = blockIdx.x; w < items && !failed; w += gridDim.x) {
+      for (long long w = pair; w < items && !failed; w += pairs) {
         int mt, nt;
         decode(w, mt, nt);
         for (int i = 0; i < kt_count; ++i, ++g) {
@@ -126,21 +175,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
             failed = 1;
             break;
           }
-          const uint32_t bar = full0 + 8 * s, sa = s0 + s * kStage;
-          mbar_expect(bar, kStage);
-          tma_2d(sa, &wmap, bar, i * kBK, mt * kBM);
-          tma_2d(sa + kABytes, &xmap, bar, i * kBK, nt * BN);
+          const uint32_t bar = leader_full0 + 8 * s, sa = s0 + s * kStage;
+          if (rank == 0) mbar_expect(full0 + 8 * s, 2 * kStage);      // both CTAs' copies
+          tma_2d_pair(sa, &wmap, bar, i * kBK, mt * 2 * kBM + (int)rank * kBM);
+          tma_2d_pair(sa + kABytes, &xmap, bar, i * kBK, nt * BN + (int)rank * (BN / 2));
         }
       }
-      // the copies in flight land before the CTA ends
-      for (long long x = (g > kStages ? g - kStages : 0); x < g; ++x)
-        if (!mbar_wait(full0 + 8 * (int)(x % kStages), (uint32_t)(x / kStages) & 1, kDrainCycles)) failed = 1;
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0 && run) {
       long long g = 0;
       int u = 0;
-      for (long long w = blockIdx.x; w < items && !failed; w += gridDim.x, ++u) {
+      for (long long w = pair; w < items && !failed; w += pairs, ++u) {
         const int b = u & 1;
         if (u >= 2 && !mbar_wait(tempty0 + 8 * b, ((u >> 1) & 1) ^ 1, wait_cycles)) {
           failed = 1;
@@ -157,36 +203,32 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
           const uint32_t sa = s0 + s * kStage;
 #pragma unroll
           for (int j = 0; j < kBK / 32; ++j)
-            mma_i8(tmem + b * BN, sw128_desc(sa + 32 * j), sw128_desc(sa + kABytes + 32 * j), idesc(BN),
-                   (i > 0 || j > 0) ? 1u : 0u);
-          mma_commit(empty0 + 8 * s);
+            mma_i8<1>(tmem + b * BN, sw128_desc(sa + 32 * j), sw128_desc(sa + kABytes + 32 * j), idesc(2 * kBM, BN),
+                      (i > 0 || j > 0) ? 1u : 0u);
+          mma_commit2(empty0 + 8 * s);
         }
         if (failed) break;
-        mma_commit(tfull0 + 8 * b);
+        mma_commit2(tfull0 + 8 * b);
       }
       // never free TMEM under a running MMA
-      mma_commit(mdone);
+      mma_commit2(mdone);
       if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
     }
-  } else {
+  } else if (run) {
     const int q = warp & 3, et = threadIdx.x - 64;       // TMEM lanes 32 q .. of this warp; epilogue thread
+    const uint32_t leader_tempty0 = map_rank(tempty0, 0);
+    T* Y = static_cast<T*>(out.Y);
     int u = 0;
-    for (long long w = blockIdx.x; w < items; w += gridDim.x, ++u) {
+    for (long long w = pair; w < items; w += pairs, ++u) {
       int mt, nt;
       decode(w, mt, nt);
-      const int b = u & 1, n0 = nt * BN, row = mt * kBM + q * 32 + lane;
+      const int b = u & 1, n0 = nt * BN, row = mt * 2 * kBM + (int)rank * kBM + q * 32 + lane;
       for (int e = et; e < BN; e += 128) {
         const bool in = n0 + e < n;
-        tok_scale[b * BN + e] = in ? xs[n0 + e] : 0.f;
-        tok_sum[b * BN + e] = in ? xsum[n0 + e] : 0;
+        tok_scale[b * BN + e] = in ? out.xs[n0 + e] : 0.f;
+        tok_sum[b * BN + e] = in ? out.xsum[n0 + e] : 0;
       }
-      float sr = 0.f;
-      int zr = 0;
-      if (row < rows) {
-        const float2 gz = *reinterpret_cast<const float2*>(grid + 2 * (long long)row);
-        sr = gz.x;
-        zr = (int)gz.y - half;
-      }
+      const Channel ch = channel(out, row);
       asm volatile("bar.sync 1, 128;" ::: "memory");
       int bad = failed;
       if (!bad) bad = !mbar_wait(tfull0 + 8 * b, (u >> 1) & 1, wait_cycles);
@@ -194,30 +236,209 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_kernel(
       if (bad) failed = 1;
       fence_after();
       if (!bad) {
+        const int cols = min(BN, n - n0);
         T* yp = Y + (long long)n0 * rows + row;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + c), v);
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + c), v);
           tmem_ld_wait();
+          if (row < rows) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (row >= rows || n0 + c + e >= n) continue;
-            const int acc = (int)v[e] - zr * tok_sum[b * BN + c + e];
-            store_y(yp + (long long)(c + e) * rows, (float)acc * sr * tok_scale[b * BN + c + e]);
+            for (int e = 0; e < 32; ++e) {
+              const int acc = (int)v[e] - ch.zero * tok_sum[b * BN + c + e];
+              if (c + e < cols) store_y(yp, (float)acc * ch.scale * tok_scale[b * BN + c + e]);
+              yp += rows;
+            }
           }
         }
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty0 + 8 * b);
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * b);
       // a warp that gave up still meets the others at the named barrier of the remaining tiles
     }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (failed && threadIdx.x == 0) {
+    set_info(info, SGPT_INFO_TIMEOUT);
+    // copies of this CTA may still be in flight on a barrier that nothing waits for any more
+    const long long t0 = clock64();
+    while (clock64() - t0 < kGraceCycles) {
+    }
+  }
+  __syncthreads();
+  cluster_sync();                               // the pair ends together: MMAs and barriers reach into both CTAs
+  if (warp == 0) tmem_free2(tmem, 2 * BN);
+}
+
+// ---------------------------------------------------- one tile, split over K
+
+constexpr int kMaxSplit = 8;                    // CTAs of a cluster that share a tile
+
+__host__ __device__ constexpr int split_stages(int bn) { return bn <= 64 ? 4 : 3; }
+__host__ __device__ constexpr int split_stage(int bn) { return kABytes + bn * kBK; }
+__host__ __device__ constexpr size_t split_smem(int bn) {
+  return (size_t)split_stages(bn) * split_stage(bn) + 1024 + 128;
+}
+// CTAs that fit on an SM together
+__host__ __device__ constexpr int split_per_sm(int bn) { return bn <= 16 ? 3 : 2; }
+static_assert(3 * (split_smem(16) + 1024) <= 233472 && 2 * (split_smem(128) + 1024) <= 233472, "CTAs per SM");
+
+template <int BN, class T>
+__global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                   const __grid_constant__ CUtensorMap xmap, int d,
+                                                                   int split, const Out out, int* info,
+                                                                   const long long wait_cycles) {
+  constexpr int kStages = split_stages(BN), kStage = split_stage(BN);
+  constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  __shared__ uint32_t tmem_slot;
+  __shared__ int failed, skip;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();                    // this CTA's part of K
+  const int tile = blockIdx.x / split;
+  const int rows = out.rows, n = out.n;
+  const int mt_count = cdiv(rows, kBM), kt_count = cdiv(d, kBK);
+  const int mt = tile % mt_count, nt = tile / mt_count;
+  const int k0 = (int)((long long)kt_count * rank / split), k1 = (int)((long long)kt_count * (rank + 1) / split);
+  const uint32_t s0 = smem_u32(smem);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, tfull = empty0 + 8 * kStages, mdone = tfull + 8;
+  if (threadIdx.x == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    failed = 0;
+    skip = info_set(info);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(mdone, 1);
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  const bool run = skip == 0;
+
+  if (warp == 0) {
+    if (lane == 0 && run) {
+      int g = 0;
+      for (int i = k0; i < k1; ++i, ++g) {
+        const int s = g % kStages;
+        if (g >= kStages && !mbar_wait(empty0 + 8 * s, ((g / kStages) & 1) ^ 1, wait_cycles)) {
+          failed = 1;
+          break;
+        }
+        const uint32_t bar = full0 + 8 * s, sa = s0 + s * kStage;
+        mbar_expect(bar, kStage);
+        tma_2d(sa, &wmap, bar, i * kBK, mt * kBM);
+        tma_2d(sa + kABytes, &xmap, bar, i * kBK, nt * BN);
+      }
+      // the copies in flight land before the CTA ends
+      for (int x = max(g - kStages, 0); x < g; ++x)
+        if (!mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, kDrainCycles)) failed = 1;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && run) {
+      for (int g = 0; g < k1 - k0; ++g) {
+        const int s = g % kStages;
+        if (!mbar_wait(full0 + 8 * s, (g / kStages) & 1, wait_cycles)) {
+          failed = 1;
+          break;
+        }
+        fence_after();
+        const uint32_t sa = s0 + s * kStage;
+#pragma unroll
+        for (int j = 0; j < kBK / 32; ++j)
+          mma_i8<0>(tmem, sw128_desc(sa + 32 * j), sw128_desc(sa + kABytes + 32 * j), idesc(kBM, BN),
+                    (g > 0 || j > 0) ? 1u : 0u);
+        mma_commit(empty0 + 8 * s);
+      }
+      if (!failed) mma_commit(tfull);
+      // never free TMEM under a running MMA
+      mma_commit(mdone);
+      if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
+    }
+  }
+  const int q = warp & 3, r = q * 32 + lane;               // epilogue warps: TMEM lane = channel in the tile
+  const int row = mt * kBM + r, n0 = nt * BN, cols = min(BN, n - n0);
+  const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+  T* Y = static_cast<T*>(out.Y);
+  bool ok = run;
+  if (warp >= 2 && run) {
+    const int bad = !mbar_wait(tfull, 0, wait_cycles);
+    if (__any_sync(0xffffffffu, bad)) {
+      failed = 1;
+      ok = false;
+    }
+    fence_after();
+  }
+  if (split == 1) {
+    if (warp >= 2 && ok) {
+      const Channel ch = channel(out, row);
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + c, v);
+        tmem_ld_wait();
+        if (row < rows) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (c + e >= cols) continue;
+            const int t = n0 + c + e;
+            const int acc = (int)v[e] - ch.zero * out.xsum[t];
+            store_y(Y + (long long)t * rows + row, (float)acc * ch.scale * out.xs[t]);
+          }
+        }
+      }
+    }
+  } else {
+    // the parts of the sum, token by token, in the ring that the products
+    // have left; each CTA of the cluster then adds up and writes its share
+    // of the tokens (int32 sums: any order gives the same bits)
+    int32_t* part = reinterpret_cast<int32_t*>(smem);      // [BN][128]
+    if (warp >= 2 && ok) {
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(c + e) * kBM + r] = (int32_t)v[e];
+      }
+    }
+    if (warp >= 2 && !ok) failed = run ? 1 : failed;
+    __syncwarp();
+    cluster_sync();
+    bool all = run;
+    for (int p = 0; p < split; ++p)
+      all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0 && ld_cluster(map_rank(smem_u32(&skip), p)) == 0;
+    if (warp >= 2 && all && row < rows) {
+      const Channel ch = channel(out, row);
+      for (int c = rank; c < cols; c += split) {
+        int acc = 0;
+        for (int p = 0; p < split; ++p) acc += ld_cluster(map_rank(s0, p) + 4 * (c * kBM + r));
+        const int t = n0 + c;
+        acc -= ch.zero * out.xsum[t];
+        store_y(Y + (long long)t * rows + row, (float)acc * ch.scale * out.xs[t]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();                                        // no CTA leaves while its sums are read
   }
   fence_before();
   __syncthreads();
   if (failed && threadIdx.x == 0) set_info(info, SGPT_INFO_TIMEOUT);
-  if (warp == 0) tmem_free(tmem, tmem_cols(BN));
+  if (warp == 0) tmem_free(tmem, kCols);
 }
 
 // int8 [rows x d], boxes of 128 bytes x `box` rows with the 128-byte swizzle.
@@ -235,42 +456,68 @@ bool map_i8(CUtensorMap* m, const int8_t* p, long long rows, long long d, int bo
 
 struct Args {
   const int8_t* Xq;
-  const float* xs;
-  const int32_t* xsum;
-  long long n;
   const int8_t* codes;
-  const float* grid;
-  int half, d, rows;
-  void* Y;
+  int d;
+  Out out;
   int* info;
   cudaStream_t st;
 };
 
-template <int BN, class T>
-cudaError_t launch(const Args& a) {
+template <class T>
+cudaError_t launch_pair(const Args& a) {
   CUtensorMap wm, xm;
-  if (!map_i8(&wm, a.codes, a.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.n, a.d, BN)) return cudaErrorInvalidValue;
+  if (!map_i8(&wm, a.codes, a.out.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.out.n, a.d, kPairN / 2))
+    return cudaErrorInvalidValue;
   static PerDevice attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(linear_i8_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_for(BN));
+    return cudaFuncSetAttribute(linear_i8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
   });
   if (e != cudaSuccess) return e;
-  const long long items = (long long)cdiv(a.rows, kBM) * cdivll(a.n, BN);
-  const int ctas = (int)std::min<long long>(items, kNumSMs);
-  linear_i8_kernel<BN, T><<<ctas, kThreads, smem_for(BN), a.st>>>(wm, xm, a.rows, a.d, (int)a.n, a.grid, a.half, a.xs,
-                                                                 a.xsum, static_cast<T*>(a.Y), a.info,
-                                                                 wait_limit_cycles());
+  const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, kPairN);
+  const int pairs = (int)std::min<long long>(items, kNumSMs / 2);
+  linear_i8_pair_kernel<T><<<2 * pairs, kThreads, kPairSmem, a.st>>>(wm, xm, a.d, a.out, a.info, wait_limit_cycles());
   count_launches(1);
   return cudaGetLastError();
 }
 
+template <int BN, class T>
+cudaError_t launch_split(const Args& a) {
+  CUtensorMap wm, xm;
+  if (!map_i8(&wm, a.codes, a.out.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.out.n, a.d, BN)) return cudaErrorInvalidValue;
+  static PerDevice attrs;
+  cudaError_t e = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(linear_i8_split_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)split_smem(BN));
+  });
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, BN);
+  const int kt = cdiv(a.d, kBK);
+  int split = 1;
+  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * split_per_sm(BN) && split * 4 <= kt) split *= 2;
+  if (tiles * split > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = split_smem(BN);
+  cfg.stream = a.st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, linear_i8_split_kernel<BN, T>, wm, xm, a.d, split, a.out, a.info, wait_limit_cycles());
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 template <class T>
 cudaError_t dispatch(const Args& a) {
-  if (a.n <= 16) return launch<16, T>(a);
-  if (a.n <= 32) return launch<32, T>(a);
-  if (a.n <= 64) return launch<64, T>(a);
-  if (a.n <= 128) return launch<128, T>(a);
-  return launch<256, T>(a);
+  const long long n = a.out.n, pair_tiles = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, kPairN);
+  if (n <= 16) return launch_split<16, T>(a);
+  if (n <= 32) return launch_split<32, T>(a);
+  if (n <= 64) return launch_split<64, T>(a);
+  if (pair_tiles >= kNumSMs / 4) return launch_pair<T>(a);
+  return launch_split<128, T>(a);
 }
 
 }  // namespace
@@ -278,7 +525,7 @@ cudaError_t dispatch(const Args& a) {
 cudaError_t launch_linear_i8(const int8_t* Xq, const float* xs, const int32_t* xsum, long long n, const int8_t* codes,
                              const float* grid, int bits, int d, int rows, void* Y, bool y_bf16, int* info,
                              cudaStream_t st) {
-  const Args a{Xq, xs, xsum, n, codes, grid, 1 << (bits - 1), d, rows, Y, info, st};
+  const Args a{Xq, codes, d, Out{grid, xs, xsum, Y, rows, (int)n, 1 << (bits - 1)}, info, st};
   return y_bf16 ? dispatch<uint16_t>(a) : dispatch<float>(a);
 }
 

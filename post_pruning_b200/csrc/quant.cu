@@ -6,16 +6,22 @@
 // row of zeros has s = 0 and q = 0. With the gate (GATED), x is
 // silu(g) * u = g / (1 + e^-g) * u, formed and kept in fp32: nothing is
 // rounded to bf16 in between.
-//   For bf16 x the codes are the exact ones: 127 x and the division's
-// operands are exact in fp32, the division rounds correctly, and a quotient
-// that is no tie cannot round onto one: with x = X 2^i and a = A 2^j (X and A
-// integers below 256, e = j - i) the distance to a tie is
-// |254 X - (2k+1) A 2^e| / (2 A 2^e) >= 1 / (2 A 2^e), at least 1/254/255 of
-// the quotient, far above the 2^-24 of the rounding.
+//   For bf16 x the codes are the exact ones. 127 x is exact in fp32. A
+// quotient that is no tie cannot round across one: with x = X 2^i and
+// a = A 2^j (X and A integers below 256, e = j - i) its distance to a tie is
+// |254 X - (2k+1) A 2^e| / (2 A 2^e), at least 1/254/255 of it. And a tie
+// Q = k + 1/2 comes out as itself: t = 127 x (1/a), with the reciprocal
+// rounded once, is within two units in the last place of Q, so the remainder
+// 127 x - t a is a small multiple of a's and t's units and exact in one fused
+// multiply-add, and t + remainder (1/a) rounds to Q (the residual step of
+// Markstein, IBM J. Res. Dev. 34, 1990). The gated x are no short numbers:
+// they take one product with the rounded 127/a.
 //   Bound by memory: 2 (gated: 4) bytes read and 1 written per element. A row
-// is read once: its group of threads holds it in registers between the
-// maximum and the codes (at most 32 elements per thread), a warp per row up
-// to 1024 elements, a CTA of 256 up to 8192, of 1024 up to 32768.
+// is read once: its threads hold it in registers between the maximum and the
+// codes. A warp takes a row up to 1024 elements, a CTA of 128 to 512 threads a
+// longer one, small enough that several rows are in flight per SM. A few long
+// rows (n <= 64, decoding) are split over clusters of eight CTAs, which
+// exchange their maxima and sums.
 //
 // quant_codes_kernel: the integer codes of weights on their rows' grid
 // (scale, zero point), less half the levels so that they fit a signed byte.
@@ -25,57 +31,88 @@
 #include "../../include/sgpt.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace sgpt {
 
 namespace {
 
-constexpr int kVec = 4;        // 16-byte vectors (8 elements) of a row per thread, at most
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+// silu(g) * u. The reciprocal instruction is off by at most one unit in the
+// last place.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-g)));
+  return g * r * u;
+}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// The code of x in a row of largest magnitude a = den / pre: k = 127 pre.
-__device__ __forceinline__ int code_of(float x, float k, float den) { return __float2int_rn(__fdiv_rn(x * k, den)); }
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-template <int NT, bool GATED>
+// Largest of the row's v (over the group of NT threads, and the cluster).
+template <int NT, int CL>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, uint32_t* shared_by_cluster) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (NT > 32) {
+    const int t = threadIdx.x;
+    if ((t & 31) == 0) red[t >> 5] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, (t & 31) < NT / 32 ? red[t & 31] : 0u);
+  }
+  if constexpr (CL > 1) {
+    if (threadIdx.x == 0) *shared_by_cluster = v;
+    ptx::cluster_sync();
+    v = 0;
+#pragma unroll
+    for (int p = 0; p < CL; ++p) v = max(v, (uint32_t)ptx::ld_cluster(ptx::map_rank(ptx::smem_u32(shared_by_cluster), p)));
+  }
+  return v;
+}
+
+// A row per group of NT threads (CL > 1: per cluster of CL CTAs of NT), at
+// most VPT vectors of 8 elements per thread.
+template <int NT, int VPT, int CL, bool GATED>
 __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     const uint16_t* __restrict__ X, const uint16_t* __restrict__ Uu, long long n, int d, long long ldx, long long ldu,
     int8_t* __restrict__ Xq, float* __restrict__ scale, int32_t* __restrict__ sums, int* info) {
   constexpr int kRows = NT == 32 ? 8 : 1;          // rows per CTA
-  constexpr int kWarps = NT / 32;
-  __shared__ uint32_t red[2][32];
-  if (cta_info_set(info)) return;
+  __shared__ uint32_t red[2][32], mine[2];
+  const int part = CL > 1 ? (int)ptx::cluster_rank() : 0;
+  bool skip = cta_info_set(info);
+  if constexpr (CL > 1) {                          // one decision for the cluster
+    if (threadIdx.x == 0) mine[1] = skip;
+    ptx::cluster_sync();
+    skip = ptx::ld_cluster(ptx::map_rank(ptx::smem_u32(&mine[1]), 0)) != 0;
+    ptx::cluster_sync();
+  }
+  if (skip) return;
   const int t = threadIdx.x % NT;
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / NT;
+  const long long row = (long long)(blockIdx.x / CL) * kRows + threadIdx.x / NT;
   if (kRows > 1 && row >= n) return;
-  const int vecs = d / 8;
+  const int vecs = d / 8, v0 = part * NT + t, step = NT * CL;
   const uint4* x4 = reinterpret_cast<const uint4*>(X + row * ldx);
   const uint4* u4 = reinterpret_cast<const uint4*>(GATED ? Uu + row * ldu : nullptr);
 
-  uint4 raw[kVec];                 // the row, bf16 (GATED: z holds it in fp32)
-  float z[GATED ? kVec * 8 : 1];
+  uint4 raw[VPT];                  // the row, bf16 (GATED: z holds it in fp32)
+  float z[GATED ? VPT * 8 : 1];
   uint32_t top = 0;                // bits of the largest magnitude; NaN and infinity compare above all numbers
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
+  for (int i = 0; i < VPT; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (t + i * NT < vecs) raw[i] = x4[t + i * NT];
+    if (v0 + i * step < vecs) raw[i] = __ldcs(x4 + v0 + i * step);
   }
   if constexpr (GATED) {
-    uint4 rawu[kVec];
+    uint4 rawu[VPT];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < VPT; ++i) {
       rawu[i] = make_uint4(0, 0, 0, 0);
-      if (t + i * NT < vecs) rawu[i] = u4[t + i * NT];
+      if (v0 + i * step < vecs) rawu[i] = __ldcs(u4 + v0 + i * step);
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < VPT; ++i) {
       const uint32_t g[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       const uint32_t u[4] = {rawu[i].x, rawu[i].y, rawu[i].z, rawu[i].w};
 #pragma unroll
@@ -89,59 +126,68 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
   } else {
     uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < VPT; ++i) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
     }
     top = max(m2 & 0xffff0000u, m2 << 16);
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (kWarps > 1) {
-    if ((t & 31) == 0) red[0][t >> 5] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, (t & 31) < kWarps ? red[0][t & 31] : 0u);
-  }
+  top = row_max<NT, CL>(top, red[0], &mine[0]);
   const bool finite = top < 0x7f800000u;
   const float a = __uint_as_float(top);
-  // 127 a stays a number: rows above 2^119 are scaled by 2^-8, exactly (what
-  // that flushes is far below half a code)
-  const float pre = a > 0x1p119f ? 0x1p-8f : 1.f;
+  // 127 a and 1 / a stay numbers: rows above 2^119 are scaled by 2^-8, rows
+  // below 2^-100 by 2^64, exactly (what the first flushes is far below half a code)
+  const float pre = a > 0x1p119f ? 0x1p-8f : a < 0x1p-100f ? 0x1p64f : 1.f;
   const float k = 127.f * pre, den = a * pre;
   const bool some = finite && top != 0u;
+  const float inv = some ? __frcp_rn(den) : 0.f;
+  const float ratio = GATED ? k * inv : 0.f;
 
   int sum = 0;
   uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    if (t + i * NT >= vecs) continue;
+  for (int i = 0; i < VPT; ++i) {
+    if (v0 + i * step >= vecs) continue;
     uint2 o = make_uint2(0, 0);
     if (some) {
       int c[8];
       if constexpr (GATED) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = code_of(z[8 * i + j], k, den);
+        for (int j = 0; j < 8; ++j) c[j] = __float2int_rn(z[8 * i + j] * ratio);
       } else {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[2 * j] = code_of(bf16_lo(w[j]), k, den);
-          c[2 * j + 1] = code_of(bf16_hi(w[j]), k, den);
+        for (int j = 0; j < 8; ++j) {
+          const float u = (j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2])) * k;
+          const float q = u * inv;
+          c[j] = __float2int_rn(fmaf(fmaf(-q, den, u), inv, q));
         }
       }
       o = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
       sum = __dp4a((int)o.x, 0x01010101, sum);
       sum = __dp4a((int)o.y, 0x01010101, sum);
     }
-    q2[t + i * NT] = o;
+    q2[v0 + i * step] = o;
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
-  if (kWarps > 1) {
+  if constexpr (NT > 32) {
     if ((t & 31) == 0) red[1][t >> 5] = (uint32_t)sum;
     __syncthreads();
-    if (t < 32) sum = __reduce_add_sync(0xffffffffu, t < kWarps ? (int)red[1][t] : 0);
+    if (t < 32) sum = __reduce_add_sync(0xffffffffu, t < NT / 32 ? (int)red[1][t] : 0);
   }
-  if (t == 0) {
+  if constexpr (CL > 1) {
+    if (t == 0) mine[1] = (uint32_t)sum;
+    __syncwarp();
+    ptx::cluster_sync();
+    if (part == 0 && t == 0) {
+      sum = 0;
+      for (int p = 0; p < CL; ++p) sum += ptx::ld_cluster(ptx::map_rank(ptx::smem_u32(&mine[1]), p));
+    }
+    __syncwarp();
+    ptx::cluster_sync();                           // no CTA leaves while its sum is read
+  }
+  if (t == 0 && part == 0) {
     scale[row] = finite ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fc00000u);
     sums[row] = sum;
     if (!finite) set_info(info, SGPT_INFO_NONFINITE);
@@ -173,17 +219,39 @@ __global__ void __launch_bounds__(256) quant_codes_kernel(const float* __restric
   if (__syncthreads_or(bad) && threadIdx.x == 0) set_info(info, SGPT_INFO_NONFINITE);
 }
 
+template <int NT, int VPT, int CL, bool GATED>
+cudaError_t launch_as(const uint16_t* X, const uint16_t* U, long long n, int d, long long ldx, long long ldu,
+                      int8_t* Xq, float* scale, int32_t* sums, int* info, cudaStream_t st) {
+  static_assert(NT == 32 || NT % 32 == 0, "whole warps");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(NT == 32 ? cdivll(n, 8) : n * CL));
+  cfg.blockDim = dim3(NT == 32 ? 256 : NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)CL, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, quant_tokens_kernel<NT, VPT, CL, GATED>, X, U, n, d, ldx, ldu, Xq, scale, sums, info);
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+constexpr int kFewRows = 64;   // rows that do not fill the SMs with a CTA each
+
 template <bool GATED>
 cudaError_t launch(const uint16_t* X, const uint16_t* U, long long n, int d, long long ldx, long long ldu, int8_t* Xq,
                    float* scale, int32_t* sums, int* info, cudaStream_t st) {
-  if (d <= 32 * 8 * kVec)
-    quant_tokens_kernel<32, GATED><<<(unsigned)cdivll(n, 8), 256, 0, st>>>(X, U, n, d, ldx, ldu, Xq, scale, sums, info);
-  else if (d <= 256 * 8 * kVec)
-    quant_tokens_kernel<256, GATED><<<(unsigned)n, 256, 0, st>>>(X, U, n, d, ldx, ldu, Xq, scale, sums, info);
-  else
-    quant_tokens_kernel<1024, GATED><<<(unsigned)n, 1024, 0, st>>>(X, U, n, d, ldx, ldu, Xq, scale, sums, info);
-  count_launches(1);
-  return cudaGetLastError();
+  const auto as = [&](auto f) { return f(X, U, n, d, ldx, ldu, Xq, scale, sums, info, st); };
+  if (d <= 1024) return as(launch_as<32, 4, 1, GATED>);
+  if (d <= 4096) return as(launch_as<128, 4, 1, GATED>);
+  if (n <= kFewRows) return as(launch_as<256, 2, 8, GATED>);
+  if (d <= 8192) return as(launch_as<256, 4, 1, GATED>);
+  if (d <= 16384) return as(launch_as<256, 8, 1, GATED>);
+  if constexpr (GATED) return as(launch_as<512, 8, 1, GATED>);
+  if (d <= 26624) return as(launch_as<256, 13, 1, false>);
+  return as(launch_as<256, 16, 1, false>);
 }
 
 }  // namespace

@@ -47,9 +47,10 @@ def _check_tokens(X, q, s, t):
     assert torch.equal(t.long(), q.long().sum(1))
 
 
-# a warp per row (to 1024), 256 threads (to 8192), 1024 threads; odd counts of 8-element vectors
-@pytest.mark.parametrize("n,d", [(1, 32), (9, 96), (1, 1024), (3, 1056), (17, 5120), (2, 8192), (5, 8224), (1, 25600),
-                                 (3, 32768), (2000, 768)])
+# both sides of every width at which more threads share a row, few rows (a cluster each above 4096) and many
+@pytest.mark.parametrize("n,d", [(1, 32), (9, 96), (1, 1024), (3, 1056), (200, 4096), (1, 4128), (17, 5120), (2, 8192),
+                                 (5, 8224), (1, 25600), (64, 32768), (65, 5120), (70, 8224), (66, 16416), (65, 26624),
+                                 (66, 26656), (65, 32768), (2000, 768)])
 def test_quant_tokens(n, d):
     g = _gen(n + d)
     X = (torch.randn(n, d, device=DEV, generator=g) * torch.exp(2 * torch.randn(d, device=DEV, generator=g))).bfloat16()
@@ -122,7 +123,8 @@ def test_non_finite_tokens_are_reported(bad, gated):
     assert pp.sync_status(info) == 3 and bool((y == 5).all())
 
 
-@pytest.mark.parametrize("n,d,strided", [(1, 64, False), (11, 768, True), (3, 5120, False), (2, 25600, True), (1, 32768, False)])
+@pytest.mark.parametrize("n,d,strided", [(1, 64, False), (11, 768, True), (3, 5120, False), (2, 25600, True), (1, 32768, False),
+                                         (65, 4128, True), (66, 8224, False), (65, 16416, True), (65, 32768, False)])
 def test_quant_tokens_silu(n, d, strided):
     g = _gen(3 * n + d)
     if strided:
