@@ -132,7 +132,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
     prefetch_map(&wmap);
     prefetch_map(&xmap);
     failed = 0;
-    skip = info_set(info);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);              // used in the first CTA
       mbar_init(empty0 + 8 * s, 1);
@@ -145,6 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
+  after_previous();
+  if (threadIdx.x == 0) skip = info_set(info);
   fence_before();
   cluster_sync();
   fence_after();
@@ -277,6 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 // ---------------------------------------------------- one tile, split over K
 
 constexpr int kMaxSplit = 8;                    // CTAs of a cluster that share a tile
+constexpr int kAhead = 8;                       // stages of codes fetched into the L2 before the predecessor has ended
 
 __host__ __device__ constexpr int split_stages(int bn) { return bn <= 64 ? 4 : 3; }
 __host__ __device__ constexpr int split_stage(int bn) { return kABytes + bn * kBK; }
@@ -285,7 +287,7 @@ __host__ __device__ constexpr size_t split_smem(int bn) {
 }
 // CTAs that fit on an SM together
 __host__ __device__ constexpr int split_per_sm(int bn) { return bn <= 16 ? 3 : 2; }
-static_assert(3 * (split_smem(16) + 1024) <= 233472 && 2 * (split_smem(128) + 1024) <= 233472, "CTAs per SM");
+static_assert(3 * (split_smem(16) + 1280) <= 233472 && 2 * (split_smem(128) + 2176) <= 233472, "CTAs per SM");
 
 template <int BN, class T>
 __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_constant__ CUtensorMap wmap,
@@ -300,6 +302,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
   __shared__ uint32_t tmem_slot;
   __shared__ int failed, skip;
+  __shared__ float tok_scale[BN];
+  __shared__ int32_t tok_sum[BN];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();                    // this CTA's part of K
   const int tile = blockIdx.x / split;
@@ -313,7 +317,6 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     prefetch_map(&wmap);
     prefetch_map(&xmap);
     failed = 0;
-    skip = info_set(info);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
@@ -323,6 +326,10 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
+  if (warp == 1 && lane == 0)
+    for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * kBM);
+  after_previous();
+  if (threadIdx.x == 0) skip = info_set(info);
   fence_before();
   __syncthreads();
   fence_after();
@@ -372,11 +379,17 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   const int q = warp & 3, r = q * 32 + lane;               // epilogue warps: TMEM lane = channel in the tile
   const int row = mt * kBM + r, n0 = nt * BN, cols = min(BN, n - n0);
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-  T* Y = static_cast<T*>(out.Y);
+  T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
+  Channel ch{0.f, 0};
   bool ok = run;
   if (warp >= 2 && run) {
-    const int bad = !mbar_wait(tfull, 0, wait_cycles);
-    if (__any_sync(0xffffffffu, bad)) {
+    for (int e = threadIdx.x - 64; e < cols; e += 128) {
+      tok_scale[e] = out.xs[n0 + e];
+      tok_sum[e] = out.xsum[n0 + e];
+    }
+    ch = channel(out, row);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (__any_sync(0xffffffffu, !mbar_wait(tfull, 0, wait_cycles))) {
       failed = 1;
       ok = false;
     }
@@ -384,20 +397,16 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   }
   if (split == 1) {
     if (warp >= 2 && ok) {
-      const Channel ch = channel(out, row);
 #pragma unroll 1
       for (int c = 0; c < cols; c += 16) {
         uint32_t v[16];
         tmem_ld16(lanes + c, v);
         tmem_ld_wait();
-        if (row < rows) {
+        if (row >= rows) continue;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (c + e >= cols) continue;
-            const int t = n0 + c + e;
-            const int acc = (int)v[e] - ch.zero * out.xsum[t];
-            store_y(Y + (long long)t * rows + row, (float)acc * ch.scale * out.xs[t]);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const float y = (float)((int)v[e] - ch.zero * tok_sum[c + e]) * ch.scale * tok_scale[c + e];
+          if (c + e < cols) store_y(Y + (long long)(c + e) * rows, y);
         }
       }
     }
@@ -416,23 +425,21 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
         for (int e = 0; e < 16; ++e) part[(c + e) * kBM + r] = (int32_t)v[e];
       }
     }
-    if (warp >= 2 && !ok) failed = run ? 1 : failed;
-    __syncwarp();
     cluster_sync();
-    bool all = run;
+    bool all = true;
     for (int p = 0; p < split; ++p)
-      all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0 && ld_cluster(map_rank(smem_u32(&skip), p)) == 0;
+      all = all && (ld_cluster(map_rank(smem_u32(&failed), p)) | ld_cluster(map_rank(smem_u32(&skip), p))) == 0;
     if (warp >= 2 && all && row < rows) {
-      const Channel ch = channel(out, row);
+      const uint32_t mine = s0 + 4 * r;
+#pragma unroll 2
       for (int c = rank; c < cols; c += split) {
         int acc = 0;
-        for (int p = 0; p < split; ++p) acc += ld_cluster(map_rank(s0, p) + 4 * (c * kBM + r));
-        const int t = n0 + c;
-        acc -= ch.zero * out.xsum[t];
-        store_y(Y + (long long)t * rows + row, (float)acc * ch.scale * out.xs[t]);
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+          if (p < split) acc += ld_cluster(map_rank(mine + 4 * kBM * c, p));
+        store_y(Y + (long long)c * rows, (float)(acc - ch.zero * tok_sum[c]) * ch.scale * tok_scale[c]);
       }
     }
-    __syncwarp();
     cluster_sync();                                        // no CTA leaves while its sums are read
   }
   fence_before();
@@ -475,9 +482,8 @@ cudaError_t launch_pair(const Args& a) {
   if (e != cudaSuccess) return e;
   const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, kPairN);
   const int pairs = (int)std::min<long long>(items, kNumSMs / 2);
-  linear_i8_pair_kernel<T><<<2 * pairs, kThreads, kPairSmem, a.st>>>(wm, xm, a.d, a.out, a.info, wait_limit_cycles());
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_after(linear_i8_pair_kernel<T>, 2 * pairs, kThreads, kPairSmem, 1, a.st, wm, xm, a.d, a.out, a.info,
+                      wait_limit_cycles());
 }
 
 template <int BN, class T>
@@ -493,21 +499,10 @@ cudaError_t launch_split(const Args& a) {
   const long long tiles = (long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, BN);
   const int kt = cdiv(a.d, kBK);
   int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * split_per_sm(BN) && split * 4 <= kt) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * split_per_sm(BN) && split * 2 <= kt) split *= 2;
   if (tiles * split > INT32_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = split_smem(BN);
-  cfg.stream = a.st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)split, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, linear_i8_split_kernel<BN, T>, wm, xm, a.d, split, a.out, a.info, wait_limit_cycles());
-  count_launches(1);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return launch_after(linear_i8_split_kernel<BN, T>, (unsigned)(tiles * split), kThreads, split_smem(BN), split, a.st, wm,
+                      xm, a.d, split, a.out, a.info, wait_limit_cycles());
 }
 
 template <class T>
@@ -517,6 +512,7 @@ cudaError_t dispatch(const Args& a) {
   if (n <= 32) return launch_split<32, T>(a);
   if (n <= 64) return launch_split<64, T>(a);
   if (pair_tiles >= kNumSMs / 4) return launch_pair<T>(a);
+  if ((long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, 128) < kNumSMs) return launch_split<64, T>(a);
   return launch_split<128, T>(a);
 }
 

@@ -20,7 +20,7 @@
 // is read once: its threads hold it in registers between the maximum and the
 // codes. A warp takes a row up to 1024 elements, a CTA of 128 to 512 threads a
 // longer one, small enough that several rows are in flight per SM. A few long
-// rows (n <= 64, decoding) are split over clusters of eight CTAs, which
+// rows (above 8192, n <= 64: decoding) are split over clusters of eight CTAs, which
 // exchange their maxima and sums.
 //
 // quant_codes_kernel: the integer codes of weights on their rows' grid
@@ -53,6 +53,9 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
 }
 
 // Largest of the row's v (over the group of NT threads, and the cluster).
+// Everything above infinity's bits is NaN's; kSkip above all says that a CTA
+// of the cluster has seen an error recorded and does nothing.
+constexpr uint32_t kSkip = 0xffffffffu;
 template <int NT, int CL>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, uint32_t* shared_by_cluster) {
   v = __reduce_max_sync(0xffffffffu, v);
@@ -63,7 +66,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, uint32_t*
     v = __reduce_max_sync(0xffffffffu, (t & 31) < NT / 32 ? red[t & 31] : 0u);
   }
   if constexpr (CL > 1) {
-    if (threadIdx.x == 0) *shared_by_cluster = v;
+    if (threadIdx.x == 0) {
+      shared_by_cluster[0] = v;
+      shared_by_cluster[1] = 0;                    // the codes' sum follows there
+    }
     ptx::cluster_sync();
     v = 0;
 #pragma unroll
@@ -81,14 +87,10 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
   constexpr int kRows = NT == 32 ? 8 : 1;          // rows per CTA
   __shared__ uint32_t red[2][32], mine[2];
   const int part = CL > 1 ? (int)ptx::cluster_rank() : 0;
-  bool skip = cta_info_set(info);
-  if constexpr (CL > 1) {                          // one decision for the cluster
-    if (threadIdx.x == 0) mine[1] = skip;
-    ptx::cluster_sync();
-    skip = ptx::ld_cluster(ptx::map_rank(ptx::smem_u32(&mine[1]), 0)) != 0;
-    ptx::cluster_sync();
-  }
-  if (skip) return;
+  ptx::let_next_start();
+  ptx::after_previous();
+  const bool skip = cta_info_set(info);
+  if (CL == 1 && skip) return;
   const int t = threadIdx.x % NT;
   const long long row = (long long)(blockIdx.x / CL) * kRows + threadIdx.x / NT;
   if (kRows > 1 && row >= n) return;
@@ -133,7 +135,11 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     }
     top = max(m2 & 0xffff0000u, m2 << 16);
   }
-  top = row_max<NT, CL>(top, red[0], &mine[0]);
+  top = row_max<NT, CL>(CL > 1 && skip ? kSkip : top, red[0], &mine[0]);
+  if (CL > 1 && top == kSkip) {                    // one decision for the cluster
+    ptx::cluster_sync();                           // no CTA leaves while its word is read
+    return;
+  }
   const bool finite = top < 0x7f800000u;
   const float a = __uint_as_float(top);
   // 127 a and 1 / a stay numbers: rows above 2^119 are scaled by 2^-8, rows
@@ -177,15 +183,10 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     if (t < 32) sum = __reduce_add_sync(0xffffffffu, t < NT / 32 ? (int)red[1][t] : 0);
   }
   if constexpr (CL > 1) {
-    if (t == 0) mine[1] = (uint32_t)sum;
-    __syncwarp();
+    // mine[1] of the first CTA was cleared before the maxima were exchanged
+    if (t == 0) ptx::add_cluster(ptx::map_rank(ptx::smem_u32(&mine[1]), 0), sum);
     ptx::cluster_sync();
-    if (part == 0 && t == 0) {
-      sum = 0;
-      for (int p = 0; p < CL; ++p) sum += ptx::ld_cluster(ptx::map_rank(ptx::smem_u32(&mine[1]), p));
-    }
-    __syncwarp();
-    ptx::cluster_sync();                           // no CTA leaves while its sum is read
+    sum = (int)mine[1];
   }
   if (t == 0 && part == 0) {
     scale[row] = finite ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fc00000u);
@@ -223,19 +224,8 @@ template <int NT, int VPT, int CL, bool GATED>
 cudaError_t launch_as(const uint16_t* X, const uint16_t* U, long long n, int d, long long ldx, long long ldu,
                       int8_t* Xq, float* scale, int32_t* sums, int* info, cudaStream_t st) {
   static_assert(NT == 32 || NT % 32 == 0, "whole warps");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(NT == 32 ? cdivll(n, 8) : n * CL));
-  cfg.blockDim = dim3(NT == 32 ? 256 : NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)CL, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = CL > 1 ? 1 : 0;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, quant_tokens_kernel<NT, VPT, CL, GATED>, X, U, n, d, ldx, ldu, Xq, scale, sums, info);
-  count_launches(1);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return launch_after(quant_tokens_kernel<NT, VPT, CL, GATED>, (unsigned)(NT == 32 ? cdivll(n, 8) : n * CL),
+                      NT == 32 ? 256 : NT, 0, CL, st, X, U, n, d, ldx, ldu, Xq, scale, sums, info);
 }
 
 constexpr int kFewRows = 64;   // rows that do not fill the SMs with a CTA each
@@ -246,8 +236,8 @@ cudaError_t launch(const uint16_t* X, const uint16_t* U, long long n, int d, lon
   const auto as = [&](auto f) { return f(X, U, n, d, ldx, ldu, Xq, scale, sums, info, st); };
   if (d <= 1024) return as(launch_as<32, 4, 1, GATED>);
   if (d <= 4096) return as(launch_as<128, 4, 1, GATED>);
-  if (n <= kFewRows) return as(launch_as<256, 2, 8, GATED>);
   if (d <= 8192) return as(launch_as<256, 4, 1, GATED>);
+  if (n <= kFewRows) return as(launch_as<256, 2, 8, GATED>);
   if (d <= 16384) return as(launch_as<256, 8, 1, GATED>);
   if constexpr (GATED) return as(launch_as<512, 8, 1, GATED>);
   if (d <= 26624) return as(launch_as<256, 13, 1, false>);

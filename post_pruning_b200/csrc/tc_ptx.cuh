@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace sgpt {
@@ -148,6 +150,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// ------------------------------------------------- programmatic dependence
+//
+// A kernel launched with launch_after() may start while its predecessor in the
+// stream still runs, and must call after_previous() in every CTA before it
+// touches anything in global memory that others write (reads of *info and
+// prefetches into the L2, which is coherent, excepted: a prefetch only). Its
+// predecessor lets it start by let_next_start() (or by ending); the
+// predecessor's results are complete and visible after after_previous() only.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// The box's bytes into the L2.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // --------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -171,6 +191,9 @@ __device__ __forceinline__ int32_t ld_cluster(uint32_t addr) {
   int32_t v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void add_cluster(uint32_t addr, int32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -222,6 +245,28 @@ inline TmaEncodeFn tma_encode_fn() {
     return nullptr;
   }();
   return fn;
+}
+
+// Launches f with clusters of `cluster` CTAs, allowed to start before its
+// predecessor in the stream has ended (see after_previous()).
+template <class... P, class... A>
+cudaError_t launch_after(void (*f)(P...), unsigned grid, int threads, size_t smem, unsigned cluster, cudaStream_t st,
+                         A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {cluster, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f, std::forward<A>(args)...);
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace sgpt

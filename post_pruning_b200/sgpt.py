@@ -10,7 +10,6 @@ missing, every call raises.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -40,7 +39,6 @@ EXPORTS = (
 )
 DRIVER_SEQUENTIAL = 0
 DRIVER_PARALLEL = 1
-_HERE_ALREADY = contextlib.nullcontext()
 
 
 class SgptError(RuntimeError):
@@ -175,13 +173,28 @@ def _dev(t: torch.Tensor, dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _on(*tensors: torch.Tensor):
-    """The device of `tensors`, which must be one, made current for a launch."""
+def _one_device(*tensors: torch.Tensor) -> int:
+    """The index of the device of `tensors`, which must be one."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
-    return _HERE_ALREADY if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return dev
+
+
+# the handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream() builds (3 us of a 10 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _enqueue(entry: str, dev: int, stream, *args):
+    """Calls a C entry whose last argument is the stream, with the tensors'
+    device current."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _enqueue(entry, dev, stream, *args)
+    _check(getattr(lib(), entry)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), entry)
 
 
 def _rowmajor(t: torch.Tensor, name: str) -> int:
@@ -430,9 +443,8 @@ def quant_codes(W: torch.Tensor, grid: torch.Tensor, codes: torch.Tensor, dev_in
     r, d = W.shape
     if grid.shape != (r, 2) or codes.shape != (r, d) or not grid.is_contiguous() or not codes.is_contiguous():
         raise ValueError("grid must be contiguous [d_out, 2] and codes contiguous [d_out, d_in]")
-    with _on(W, grid, codes, dev_info):
-        _check(lib().sgpt_quant_codes(_ptr(W), r, d, ldw, _ptr(grid), qbits, _ptr(codes), _ptr(dev_info),
-                                      _stream(stream)), "sgpt_quant_codes")
+    _enqueue("sgpt_quant_codes", _one_device(W, grid, codes, dev_info), stream, _ptr(W), r, d, ldw, _ptr(grid), qbits,
+             _ptr(codes), _ptr(dev_info))
 
 
 def _token_outputs(n: int, d: int, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor):
@@ -453,9 +465,8 @@ def quant_tokens(X: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: t
     ldx = _row_stride(X, "X")
     n, d = X.shape
     _token_outputs(n, d, Xq, scale, sums)
-    with _on(X, Xq, scale, sums, dev_info):
-        _check(lib().sgpt_quant_tokens(_ptr(X), n, d, ldx, _ptr(Xq), _ptr(scale), _ptr(sums), _ptr(dev_info),
-                                       _stream(stream)), "sgpt_quant_tokens")
+    _enqueue("sgpt_quant_tokens", _one_device(X, Xq, scale, sums, dev_info), stream, _ptr(X), n, d, ldx, _ptr(Xq),
+             _ptr(scale), _ptr(sums), _ptr(dev_info))
 
 
 def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor,
@@ -469,9 +480,8 @@ def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale:
     if U.shape != (n, d):
         raise ValueError("G and U must have the same shape")
     _token_outputs(n, d, Xq, scale, sums)
-    with _on(G, U, Xq, scale, sums, dev_info):
-        _check(lib().sgpt_quant_tokens_silu(_ptr(G), _ptr(U), n, d, ldg, ldu, _ptr(Xq), _ptr(scale),
-                                            _ptr(sums), _ptr(dev_info), _stream(stream)), "sgpt_quant_tokens_silu")
+    _enqueue("sgpt_quant_tokens_silu", _one_device(G, U, Xq, scale, sums, dev_info), stream, _ptr(G), _ptr(U), n, d, ldg,
+             ldu, _ptr(Xq), _ptr(scale), _ptr(sums), _ptr(dev_info))
 
 
 def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: torch.Tensor, grid: torch.Tensor,
@@ -492,9 +502,8 @@ def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: 
         raise ValueError("codes must be [d_out, d_in], grid [d_out, 2] and Y [n, d_out]")
     if not (codes.is_contiguous() and grid.is_contiguous() and Y.is_contiguous()):
         raise ValueError("codes, grid and Y must be contiguous")
-    with _on(Xq, scale, sums, codes, grid, Y, dev_info):
-        _check(lib().sgpt_linear_i8(_ptr(Xq), _ptr(scale), _ptr(sums), n, _ptr(codes), _ptr(grid), qbits, d_in, d_out,
-                                    _ptr(Y), y_bf16, _ptr(dev_info), _stream(stream)), "sgpt_linear_i8")
+    _enqueue("sgpt_linear_i8", _one_device(Xq, scale, sums, codes, grid, Y, dev_info), stream, _ptr(Xq), _ptr(scale),
+             _ptr(sums), n, _ptr(codes), _ptr(grid), qbits, d_in, d_out, _ptr(Y), y_bf16, _ptr(dev_info))
 
 
 def _heads(t: torch.Tensor, name: str) -> int:
@@ -520,10 +529,9 @@ def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.
         raise ValueError("Q and O must be [n_tok, heads, width], K and V [n_tok, kv_heads, width]")
     if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be contiguous [n_seq + 1]")
-    with _on(Q, K, V, O, offsets, dev_info):
-        _check(lib().sgpt_attention(_ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, _ptr(offsets), offsets.shape[0] - 1, n,
-                                    heads, kv_heads, width, width ** -0.5 if scale is None else scale, _ptr(O), ldo,
-                                    _ptr(dev_info), _stream(stream)), "sgpt_attention")
+    _enqueue("sgpt_attention", _one_device(Q, K, V, O, offsets, dev_info), stream, _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv,
+             _ptr(offsets), offsets.shape[0] - 1, n, heads, kv_heads, width, width ** -0.5 if scale is None else scale,
+             _ptr(O), ldo, _ptr(dev_info))
 
 
 def mlp_block_workspace(hidden: int, inter: int, n_tok: int, device="cuda") -> torch.Tensor:
