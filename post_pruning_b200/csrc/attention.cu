@@ -84,6 +84,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Two fp32 in one 64-bit register, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 pair_to(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Largest of 32 scores and a.
+__device__ __forceinline__ float max32(const uint32_t (&s)[32], float a) {
+  float m[4] = {a, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m[x] = max3(m[x], __uint_as_float(s[i + 2 * x]), __uint_as_float(s[i + 2 * x + 1]));
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// Scores of 64 keys after column r of them become -inf.
+__device__ __forceinline__ void mask64(uint32_t (&a)[32], uint32_t (&b)[32], int r) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i > r) a[i] = 0xff800000u;
+    if (i + 32 > r) b[i] = 0xff800000u;
+  }
+}
+
 struct Shape {
   long long ldo;             // elements between rows of O
   int n_tok, n_seq, heads, group;
@@ -149,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   const uint32_t s0 = smem_u32(smem);
   const uint32_t ring = s0 + 2 * kTile;
   const uint32_t qfull = smem_u32(bars), full0 = qfull + 16, empty0 = full0 + 8 * kStages;
-  const uint32_t sfull = empty0 + 8 * kStages, pfull = sfull + 16, ofull = pfull + 16, mdone = ofull + 16;
+  const uint32_t sfull = empty0 + 8 * kStages, pfull = sfull + 16, ofull = pfull + 32, mdone = ofull + 16;
   if (threadIdx.x == 0) {
     prefetch_map(&qmap);
     prefetch_map(&kmap);
@@ -158,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     for (int h = 0; h < 2; ++h) {
       mbar_init(qfull + 8 * h, 1);
       mbar_init(sfull + 8 * h, 1);
-      mbar_init(pfull + 8 * h, 4);
+      mbar_init(pfull + 16 * h, 4);             // the weights of the block's first 64 keys
+      mbar_init(pfull + 16 * h + 8, 4);         // and of its last 64
       mbar_init(ofull + 8 * h, 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -175,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int hu = blockIdx.x % head_units;
 
   // tile h: its head, its first row in the sequence, its key blocks
@@ -217,22 +263,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       fence_after();
       return ok;
     };
-    auto slot = [&](int g) { return ring + (g % kStages) * kTile; };
     auto wait_slot = [&](int g) { return wait(full0 + 8 * (g % kStages), (g / kStages) & 1); };
+    const uint64_t q_desc = sw128_desc(s0), k_desc = sw128_desc(ring), v_desc = sw128_desc(ring, kBox);
     auto score = [&](int h, int g) {                       // S_h = Q_h K^T
-      if (lane == 0) {
+      if (elect_one()) {
+        const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)((g % kStages) * kTile >> 4);
+        const uint32_t acc = tmem + h * kT;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kBox + 32 * (ks & 3);
-          mma_ss(tmem + h * kT, sw128_desc(s0 + h * kTile + off), sw128_desc(slot(g) + off), idesc(kT, false), ks > 0);
+          const uint64_t off = ((ks >> 2) * kBox + 32 * (ks & 3)) >> 4;
+          mma_ss(acc, qd + off, kd + off, idesc(kT, false), ks > 0);
         }
         mma_commit(sfull + 8 * h);
       }
+      __syncwarp();
+    };
+    auto signal = [&](uint32_t bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
     };
     if (wait_slot(0)) {
       for (int h = 0; h < 2; ++h)
         if (blocks_of(h) && wait(qfull + 8 * h, 0)) score(h, 0);
-      if (lane == 0) mma_commit(empty0);
+      signal(empty0);
     }
     const int ragged = len % kT;                           // keys of the sequence's last block (0: all)
     for (int j = 0; j < nb && ok; ++j) {
@@ -251,39 +304,43 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       for (int h = 0; h < 2 && ok; ++h) {
         const int mine = h ? nb1 : nb0;
         if (j >= mine) continue;
-        if (!wait(pfull + 8 * h, j & 1)) break;
-        if (lane == 0) {
+        const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
+        for (int half = 0; half < 2 && ok; ++half) {
+          if (!wait(pfull + 16 * h + 8 * half, j & 1)) break;
+          if (elect_one()) {
+            const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT + 32 * half;
+            const uint64_t vh = vd + (uint64_t)(2048 * 4 * half >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kT / 16; ++ks)
-            mma_ts(tmem + 2 * kT + h * kT, tmem + h * kT + 8 * ks, sw128_desc(slot(gv) + 2048 * ks, kBox),
-                   idesc(D, true), j > 0 || ks > 0);
+            for (int x = 0; x < 4; ++x)
+              mma_ts(acc, pd + 8 * x, vh + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j + half > 0));
+          }
+          __syncwarp();
         }
+        if (!ok) break;
         if (j + 1 < mine) {
           if (!wait_slot(gk)) break;
           score(h, gk);
-        } else if (lane == 0) {
-          mma_commit(ofull + 8 * h);
+        } else {
+          signal(ofull + 8 * h);
         }
       }
       if (!ok) break;
-      if (lane == 0) {
-        mma_commit(empty0 + 8 * (gv % kStages));
-        if (j + 1 < nb) mma_commit(empty0 + 8 * (gk % kStages));
-      }
+      signal(empty0 + 8 * (gv % kStages));
+      if (j + 1 < nb) signal(empty0 + 8 * (gk % kStages));
     }
     if (!ok) failed = 1;
     // never free TMEM under a running MMA
-    if (lane == 0) {
-      mma_commit(mdone);
-      if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
-    }
+    signal(mdone);
+    if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
   } else {
     const int h = warp >> 2, q = warp & 3;
     const int mine = h ? nb1 : nb0;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t ts = tmem + lanes + h * kT, to = tmem + lanes + 2 * kT + h * kT;
     const int r = q * 32 + lane, row = row_of(h) + r;      // row in the tile and in the sequence
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY;
+    uint64_t l2[2] = {0, 0};                               // the row's sum, in four parts
+    const uint64_t c2 = pair_of(sh.c, sh.c);
     bool ok = true;
     for (int j = 0; j < mine && ok; ++j) {
       if (__any_sync(0xffffffffu, !mbar_wait(sfull + 8 * h, j & 1, wait_cycles))) {
@@ -291,57 +348,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         break;
       }
       fence_after();
+      const bool diagonal = j == mine - 1;
       uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
+      tmem_ld32(ts, s[0]);
+      tmem_ld32(ts + 32, s[1]);
       tmem_ld_wait();
-      float top = -INFINITY;
-      if (j == mine - 1) {                                 // the diagonal block
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i > r) s[i / 32][i % 32] = 0xff800000u;
-      }
-#pragma unroll
-      for (int i = 0; i < 128; ++i) top = fmaxf(top, __uint_as_float(s[i / 32][i % 32]));
+      tmem_ld32(ts + 64, s[2]);
+      tmem_ld32(ts + 96, s[3]);
+      if (diagonal) mask64(s[0], s[1], r);
+      float top = max32(s[1], max32(s[0], -INFINITY));
+      tmem_ld_wait();
+      if (diagonal) mask64(s[2], s[3], r - 64);
+      top = max32(s[3], max32(s[2], top));
       const bool grow = j == 0 || (top - m) * sh.c > kGrow;
-      const float mnew = grow ? top : m;
       if (__any_sync(0xffffffffu, grow)) {
-        const float alpha = grow ? ex2((m - mnew) * sh.c) : 1.f;
+        const float mnew = grow ? top : m;
         if (j > 0) {
-          l *= alpha;
+          const float alpha = ex2((m - mnew) * sh.c);      // 1 where the maximum stays
+          const uint64_t a2 = pair_of(alpha, alpha);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) l2[x] = fma2(l2[x], a2, 0);
 #pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * i, o);
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * i, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(to + 32 * i, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(to + 16 * i, o);
           }
         }
         m = mnew;
       }
       const float mc = m * sh.c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t mc2 = pair_of(-mc, -mc);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int i = 64 * half + 2 * e;
-          const float a = ex2(fmaf(__uint_as_float(s[i / 32][i % 32]), sh.c, -mc));
-          const float b = ex2(fmaf(__uint_as_float(s[i / 32][i % 32 + 1]), sh.c, -mc));
-          sum[e & 3] += a + b;
+          const float2 x = pair_to(
+              fma2(pair_of(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2, mc2));
+          const float a = ex2(x.x), b = ex2(x.y);
+          l2[e & 1] = add2(l2[e & 1], pair_of(a, b));
           p[e] = pack_bf16(a, b);
         }
         tmem_st32(ts + 32 * half, p);
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + 16 * h + 8 * half);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pfull + 8 * h);
     }
+    const float2 la = pair_to(l2[0]), lb = pair_to(l2[1]);
+    const float l = (la.x + la.y) + (lb.x + lb.y);
     if (mine && ok && __any_sync(0xffffffffu, !mbar_wait(ofull + 8 * h, 0, wait_cycles))) ok = false;
     if (!ok) failed = 1;
     if (mine && ok) {

@@ -109,6 +109,15 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo_bytes
   return d;
 }
 
+// One thread of the (converged) warp. What it issues to the tensor cores
+// takes its operands from uniform registers: descriptors are formed once and
+// advanced by constants, else the issue of an MMA costs more than the MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // 32 lanes x 32 columns of 32 bits, without the wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
