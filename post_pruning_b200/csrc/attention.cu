@@ -7,13 +7,16 @@
 // rounded to bf16 for the second product (relative to the running maximum,
 // so to 2^-9 of each weight; the sum l_i takes them unrounded).
 //
-// A CTA owns two 128-row query tiles: the same rows of two heads that share
-// a key/value head, or, where the group of heads is odd, two consecutive
-// tiles of one head. Both run over the same K and V blocks of 128 keys, so
-// while one tile's four softmax warps exponentiate, the tensor cores work for
-// the other tile. Warp 8 loads Q and a ring of K and V blocks by TMA, warp 9
-// issues the products: S = Q K^T into 128 TMEM columns per tile, then, once
-// the softmax warps have replaced S by the bf16 weights in the same columns,
+// A unit of work is two 128-row query tiles: the same rows of two heads that
+// share a key/value head, or, where the group of heads is odd, two
+// consecutive tiles of one head. Both run over the same K and V blocks of 128
+// keys, so while one tile's four softmax warps exponentiate, the tensor cores
+// work for the other tile. CTAs are persistent and take the units of CTAs
+// that have not started yet (the longest of a sequence first), so a unit's
+// operands load under the one before it. Warp 8 finds the units and loads Q
+// and a ring of K and V blocks by TMA, warp 9 issues the products:
+// S = Q K^T into 128 TMEM columns per tile, then, as the softmax warps
+// replace S by the bf16 weights in the same columns, half a block at a time,
 // O += P V with P read from TMEM, followed by the next S.
 //   The running maximum is only raised when a row's maximum has grown by more
 // than 2^8 in the exponent's base (weights up to 256 are as exact as weights
@@ -39,15 +42,19 @@ namespace {
 using namespace ptx;
 
 constexpr int kT = 128;                         // query rows per tile, keys per block
-constexpr int kThreads = 320;                   // 2 x 4 softmax warps, TMA, MMA
+constexpr int kThreads = 384;                   // 2 x 4 softmax warps, TMA, MMA, two idle
+// registers a thread after the split: 2 x 216 + 72 = 3 x 168, what the block is launched with
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kBox = kT * 128;                  // 16 KB: 128 rows x 64 bf16
+constexpr int kFree = 8;                        // barriers that free ring slots, more than ring slots
 constexpr float kGrow = 8.f;                    // exponent growth that moves the running maximum
 
 __host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBox; }
 __host__ __device__ constexpr int stages_for(int D) { return D == 128 ? 5 : 8; }
 __host__ __device__ constexpr size_t smem_for(int D) {
-  return (size_t)(2 + stages_for(D)) * tile_bytes(D) + 1024 + 256;
+  return (size_t)(2 + stages_for(D)) * tile_bytes(D) + 1024 + 512;
 }
+static_assert(kFree >= stages_for(128) && kFree >= stages_for(64) && 8 * (22 + kFree + stages_for(64)) <= 512, "barriers");
 static_assert(smem_for(128) <= 232448, "dynamic shared memory per CTA");
 
 constexpr uint32_t kTmemCols = 512;             // S0, S1 (P over them), O0, O1 at 128 columns each
@@ -129,11 +136,90 @@ __device__ __forceinline__ void mask64(uint32_t (&a)[32], uint32_t (&b)[32], int
   }
 }
 
+// The weights exp2(c s - mc) of 64 scores, as bf16 pairs, and their sums.
+__device__ __forceinline__ void weights(const uint32_t (&a)[32], const uint32_t (&b)[32], uint64_t c2, float mc,
+                                        uint32_t (&p)[32], uint64_t (&sum)[2]) {
+  const uint64_t mc2 = pair_of(-mc, -mc);
+  sum[0] = sum[1] = 0;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t lo = e < 16 ? a[2 * e] : b[2 * e - 32], hi = e < 16 ? a[2 * e + 1] : b[2 * e - 31];
+    const float2 x = pair_to(fma2(pair_of(__uint_as_float(lo), __uint_as_float(hi)), c2, mc2));
+    const float u = ex2(x.x), v = ex2(x.y);
+    sum[e & 1] = add2(sum[e & 1], pair_of(u, v));
+    p[e] = pack_bf16(u, v);
+  }
+}
+
 struct Shape {
   long long ldo;             // elements between rows of O
   int n_tok, n_seq, heads, group;
-  int pair;                  // 1: a CTA's two tiles are two heads of one group; 0: two row tiles of one head
+  int pair;                  // 1: a unit's two tiles are two heads of one group; 0: two row tiles of one head
+  int wide;                  // 1: rows of O start on 32-byte boundaries
   float c;                   // scale * log2(e)
+};
+
+// A unit of work: two tiles. len == 0 ends the CTA.
+struct Work {
+  int first, len, unit, head_unit;
+  __device__ int head(const Shape& sh, int h) const { return sh.pair ? 2 * head_unit + h : head_unit; }
+  // tile h's first row in the sequence, and its key blocks
+  __device__ int row(const Shape& sh, int h) const { return sh.pair ? unit * kT : (2 * unit + h) * kT; }
+  __device__ int blocks(const Shape& sh, int h) const { return row(sh, h) < len ? row(sh, h) / kT + 1 : 0; }
+};
+
+// The unit `index` of the launch, by a whole warp. A sequence's offsets are
+// used only if they lie inside the packed rows.
+__device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lane) {
+  const int head_units = sh.pair ? sh.heads / 2 : sh.heads;
+  const int unit_rows = sh.pair ? kT : 2 * kT;
+  const int unit = index / head_units;
+  Work w{0, 0, 0, index % head_units};
+  int before = 0;
+  for (int b0 = 0; b0 < sh.n_seq; b0 += 32) {
+    const int b = b0 + lane;
+    int first = 0, len = 0;
+    if (b < sh.n_seq) {
+      first = cu[b];
+      const int end = cu[b + 1];
+      len = first >= 0 && end >= first && end <= sh.n_tok ? end - first : 0;
+    }
+    const int units = cdiv(len, unit_rows);
+    int upto = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int at = unit - (before + upto - units);          // in this lane's sequence
+    const uint32_t mine = __ballot_sync(0xffffffffu, at >= 0 && at < units);
+    if (mine) {
+      const int src = __ffs(mine) - 1;
+      w.first = __shfl_sync(0xffffffffu, first, src);
+      w.len = __shfl_sync(0xffffffffu, len, src);
+      w.unit = __shfl_sync(0xffffffffu, units - 1 - at, src);      // the longest rows of keys first
+      return w;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return w;
+}
+
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// One wait's count on a barrier: the n-th wait takes parity n & 1.
+struct Phase {
+  uint32_t n = 0;
+  __device__ uint32_t next() { return n++ & 1u; }
 };
 
 template <int D>
@@ -146,55 +232,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * kTile);
+  __shared__ __align__(16) uint32_t answer[4];
   __shared__ uint32_t tmem_slot;
   __shared__ int failed;
-  __shared__ int where[3];                       // first row, length, unit of the sequence
-  if (cta_info_set(info)) return;
+  __shared__ Work work[2];
+  __shared__ int group_of[kStages];              // producer's: what frees each ring slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head_units = sh.pair ? sh.heads / 2 : sh.heads;
-  const int unit_rows = sh.pair ? kT : 2 * kT;
-
-  if (blockIdx.x == 0) {                         // every offset is checked once
-    bool bad = false;
-    for (int b = threadIdx.x; b < sh.n_seq; b += kThreads) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
-    if (__syncthreads_or(bad) && threadIdx.x == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
-  }
-  if (warp == 0) {
-    // the sequence that holds this unit of rows; a sequence's offsets are
-    // used only if they lie inside the packed rows
-    const int unit = blockIdx.x / head_units;
-    int before = 0;
-    if (lane == 0) where[1] = 0;
-    __syncwarp();
-    for (int b0 = 0; b0 < sh.n_seq; b0 += 32) {
-      const int b = b0 + lane;
-      int first = 0, len = 0;
-      if (b < sh.n_seq) {
-        first = cu[b];
-        const int end = cu[b + 1];
-        len = first >= 0 && end >= first && end <= sh.n_tok ? end - first : 0;
-      }
-      const int units = cdiv(len, unit_rows);
-      int upto = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const bool mine = unit >= before + upto - units && unit < before + upto;
-      if (mine) {
-        where[0] = first;
-        where[1] = len;
-        where[2] = units - 1 - (unit - (before + upto - units));   // the longest rows of keys first
-      }
-      if (__any_sync(0xffffffffu, mine)) break;
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
   const uint32_t s0 = smem_u32(smem);
   const uint32_t ring = s0 + 2 * kTile;
-  const uint32_t qfull = smem_u32(bars), full0 = qfull + 16, empty0 = full0 + 8 * kStages;
-  const uint32_t sfull = empty0 + 8 * kStages, pfull = sfull + 16, ofull = pfull + 32, mdone = ofull + 16;
+  // [2]: one per tile or per work slot
+  const uint32_t qfull = smem_u32(bars), qempty = qfull + 16, sfull = qempty + 16, ofull = sfull + 16;
+  const uint32_t pfull = ofull + 16;             // [2][2]: a block's first 64 keys, its last 64
+  const uint32_t wfull = pfull + 32, wempty = wfull + 16;
+  const uint32_t full0 = wempty + 16, free0 = full0 + 8 * kStages;    // [kStages], [kFree]
+  const uint32_t vask = free0 + 8 * kFree, vready = vask + 8, stolen = vready + 8, mdone = stolen + 8;
   if (threadIdx.x == 0) {
     prefetch_map(&qmap);
     prefetch_map(&kmap);
@@ -202,214 +253,303 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     failed = 0;
     for (int h = 0; h < 2; ++h) {
       mbar_init(qfull + 8 * h, 1);
+      mbar_init(qempty + 8 * h, 1);
       mbar_init(sfull + 8 * h, 1);
-      mbar_init(pfull + 16 * h, 4);             // the weights of the block's first 64 keys
-      mbar_init(pfull + 16 * h + 8, 4);         // and of its last 64
       mbar_init(ofull + 8 * h, 1);
+      mbar_init(pfull + 16 * h, 4);
+      mbar_init(pfull + 16 * h + 8, 4);
+      mbar_init(wfull + 8 * h, 1);
+      mbar_init(wempty + 8 * h, 10);             // eight softmax warps, the MMA warp, the V tail warp
     }
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
-    }
+    for (int s = 0; s < kStages; ++s) mbar_init(full0 + 8 * s, 1);
+    for (int s = 0; s < kFree; ++s) mbar_init(free0 + 8 * s, 1);
+    mbar_init(vask, 1);
+    mbar_init(vready, 1);
+    mbar_init(stolen, 1);
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
-  __syncthreads();
-  const int first = where[0], len = where[1], unit = where[2];
-  if (len == 0) return;                          // a CTA past the last unit
+  after_previous();
+  if (cta_info_set(info)) return;
+  if (blockIdx.x == 0) {                         // every offset is checked once
+    bool bad = false;
+    for (int b = threadIdx.x; b < sh.n_seq; b += kThreads) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
+    if (__syncthreads_or(bad) && threadIdx.x == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
+  }
   if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  const int hu = blockIdx.x % head_units;
 
-  // tile h: its head, its first row in the sequence, its key blocks
-  auto head_of = [&](int h) { return sh.pair ? 2 * hu + h : hu; };
-  auto row_of = [&](int h) { return unit * unit_rows + (sh.pair ? 0 : h * kT); };
-  auto blocks_of = [&](int h) { return row_of(h) < len ? row_of(h) / kT + 1 : 0; };
-  const int nb0 = blocks_of(0), nb1 = blocks_of(1), nb = max(nb0, nb1);
-
-  if (warp == 8) {
-    if (lane == 0) {
-      const int kvh = head_of(0) / sh.group;
-      for (int h = 0; h < 2; ++h) {
-        if (!blocks_of(h)) continue;
-        mbar_expect(qfull + 8 * h, kTile);
-        for (int x = 0; x < D / 64; ++x)
-          tma_3d(s0 + h * kTile + x * kBox, &qmap, qfull + 8 * h, 64 * x, head_of(h), first + row_of(h));
-      }
-      int g = 0;                                 // ring slots used: K0 V0 K1 V1 ...
-      for (; g < 2 * nb; ++g) {
-        const int s = g % kStages;
-        if (g >= kStages && !mbar_wait(empty0 + 8 * s, ((g / kStages) & 1) ^ 1, wait_cycles)) {
-          failed = 1;
-          break;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // Units of work, one after the other, and their operands. The next
+      // unit's index is asked for while this one's operands are loaded.
+      int index = blockIdx.x;
+      uint32_t g = 0, units = 0, groups = 0;     // ring slots, units and groups of slots so far
+      uint32_t q_used[2] = {0, 0};
+      bool ok = true, asked = false;
+      Phase answers;
+      while (ok) {
+        const Work w = index < 0 ? Work{0, 0, 0, 0} : find_work(sh, cu, index, lane);
+        if (index >= 0) {
+          if (lane == 0) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the last answer has been read
+            mbar_expect(stolen, 16);
+            steal_cta(smem_u32(answer), stolen);
+          }
+          asked = true;
         }
-        mbar_expect(full0 + 8 * s, kTile);
-        for (int x = 0; x < D / 64; ++x)
-          tma_3d(ring + s * kTile + x * kBox, (g & 1) ? &vmap : &kmap, full0 + 8 * s, 64 * x, kvh, first + (g >> 1) * kT);
+        if (index < 0 || w.len) {
+          const int slot = units & 1;
+          if (lane == 0) {
+            if (units >= 2 && !mbar_wait(wempty + 8 * slot, (units / 2 - 1) & 1, wait_cycles)) ok = false;
+            if (ok) {
+              work[slot] = w;
+              mbar_arrive(wfull + 8 * slot);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          ++units;
+        }
+        if (index < 0 || !ok) break;
+        if (w.len && lane == 0) {
+          const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
+          const int kvh = w.head(sh, 0) / sh.group;
+          for (int x = 0; x < 2 * nb && ok; ++x, ++g) {             // K0 V0 K1 V1 ...
+            const uint32_t s = g % kStages;
+            if (g >= kStages) {
+              const uint32_t f = group_of[s];
+              if (!mbar_wait(free0 + 8 * (f % kFree), (f / kFree) & 1, wait_cycles)) {
+                ok = false;
+                break;
+              }
+            }
+            group_of[s] = groups + (x + 1) / 2;                      // K0 | V0 K1 | V1 K2 | ... | the last V
+            mbar_expect(full0 + 8 * s, kTile);
+            for (int c = 0; c < D / 64; ++c)
+              tma_3d(ring + s * kTile + c * kBox, (x & 1) ? &vmap : &kmap, full0 + 8 * s, 64 * c, kvh, w.first + (x >> 1) * kT);
+            if (x == 0) {
+              for (int h = 0; h < 2 && ok; ++h) {
+                if (!(h ? nb1 : nb0)) continue;
+                if (q_used[h] && !mbar_wait(qempty + 8 * h, (q_used[h] - 1) & 1, wait_cycles)) {
+                  ok = false;
+                  break;
+                }
+                ++q_used[h];
+                mbar_expect(qfull + 8 * h, kTile);
+                for (int c = 0; c < D / 64; ++c)
+                  tma_3d(s0 + h * kTile + c * kBox, &qmap, qfull + 8 * h, 64 * c, w.head(sh, h), w.first + w.row(sh, h));
+              }
+            }
+          }
+          groups += nb + 1;
+        }
+        __syncwarp();
+        const uint32_t parity = answers.next();
+        bool got = mbar_wait(stolen, parity, wait_cycles);
+        if (!got) mbar_wait(stolen, parity, kDrainCycles);
+        asked = false;
+        ok = __all_sync(0xffffffffu, ok && got);
+        index = stolen_cta(smem_u32(answer));
       }
-      // the copies in flight land before the CTA ends
-      for (int h = 0; h < 2; ++h)
-        if (blocks_of(h) && !mbar_wait(qfull + 8 * h, 0, kDrainCycles)) failed = 1;
-      for (int x = max(g - kStages, 0); x < g; ++x)
-        if (!mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, kDrainCycles)) failed = 1;
+      if (!ok && lane == 0) {
+        failed = 1;
+        // what is still in flight lands before the CTA ends
+        if (asked) mbar_wait(stolen, answers.next(), kDrainCycles);
+        for (int h = 0; h < 2; ++h)
+          if (q_used[h]) mbar_wait(qfull + 8 * h, (q_used[h] - 1) & 1, kDrainCycles);
+        for (uint32_t x = g > kStages ? g - kStages : 0; x < g; ++x)
+          mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, kDrainCycles);
+      }
+    } else if (warp == 9) {
+      if (elect_one()) {
+        const uint64_t q_desc = sw128_desc(s0), k_desc = sw128_desc(ring), v_desc = sw128_desc(ring, kBox);
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, wait_cycles)) ok = false;
+          fence_after();
+          return ok;
+        };
+        uint32_t g = 0, groups = 0;
+        Phase qn[2], pn[2], vn;
+        auto wait_slot = [&](uint32_t x) { return wait(full0 + 8 * (x % kStages), (x / kStages) & 1); };
+        auto free_group = [&] {
+          mma_commit(free0 + 8 * (groups % kFree));
+          ++groups;
+        };
+        auto score = [&](int h, uint32_t x, bool last) {   // S_h = Q_h K^T
+          const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)((x % kStages) * kTile >> 4);
+          const uint32_t acc = tmem + h * kT;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t off = ((ks >> 2) * kBox + 32 * (ks & 3)) >> 4;
+            mma_ss(acc, qd + off, kd + off, idesc(kT, false), ks > 0);
+          }
+          mma_commit(sfull + 8 * h);
+          if (last) mma_commit(qempty + 8 * h);
+        };
+        for (uint32_t u = 0; ok; ++u) {
+          if (!wait(wfull + 8 * (u & 1), (u >> 1) & 1)) break;
+          const Work w = work[u & 1];
+          mbar_arrive(wempty + 8 * (u & 1));
+          if (!w.len) break;
+          const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
+          if (!wait_slot(g)) break;
+          for (int h = 0; h < 2; ++h)
+            if ((h ? nb1 : nb0) && wait(qfull + 8 * h, qn[h].next())) score(h, g, (h ? nb1 : nb0) == 1);
+          if (!ok) break;
+          free_group();
+          for (int j = 0; j < nb; ++j) {
+            const uint32_t gv = g + 2 * j + 1, gk = gv + 1;
+            if (!wait_slot(gv)) break;
+            if (j == w.len / kT) {                         // the sequence ends inside this block
+              mbar_arrive(vask);
+              if (!wait(vready, vn.next())) break;
+            }
+            const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int mine = h ? nb1 : nb0;
+              if (j >= mine || !ok) continue;
+              const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT, par = pn[h].next();
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                if (!wait(pfull + 16 * h + 8 * half, par)) break;
+#pragma unroll
+                for (int x = 4 * half; x < 4 * half + 4; ++x)
+                  mma_ts(acc, pd + 8 * x, vd + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j > 0));
+              }
+              if (j + 1 < mine) {
+                if (wait_slot(gk)) score(h, gk, j + 2 == mine);
+              } else {
+                mma_commit(ofull + 8 * h);
+              }
+            }
+            if (!ok) break;
+            free_group();
+          }
+          g += 2 * nb;
+        }
+        if (!ok) failed = 1;
+        // never free TMEM under a running MMA
+        mma_commit(mdone);
+        if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
+      }
+    } else if (warp == 10) {
+      // Zeroes the rows of V after the end of a sequence in the block that
+      // holds it: their weights are zero, but zero times a NaN is not.
+      uint32_t g = 0;
+      Phase asked;
+      for (uint32_t u = 0;; ++u) {
+        if (__any_sync(0xffffffffu, !mbar_wait(wfull + 8 * (u & 1), (u >> 1) & 1, wait_cycles))) break;
+        const Work w = work[u & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wempty + 8 * (u & 1));
+        if (!w.len) break;
+        const int nb = max(w.blocks(sh, 0), w.blocks(sh, 1)), keys = w.len % kT;
+        if (keys && nb - 1 == w.len / kT) {
+          const uint32_t s = (g + 2 * nb - 1) % kStages;
+          if (__any_sync(0xffffffffu, !mbar_wait(vask, asked.next(), wait_cycles))) break;
+          for (int c = 0; c < D / 64; ++c)
+            for (int i = keys * 8 + lane; i < kT * 8; i += 32)
+              *reinterpret_cast<uint4*>(smem + (2 + s) * kTile + c * kBox + 16 * i) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(vready);
+        }
+        g += 2 * nb;
+      }
     }
-  } else if (warp == 9) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int h = warp >> 2, q = warp & 3;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t ts = tmem + lanes + h * kT, to = tmem + lanes + 2 * kT + h * kT;
+    const int r = q * 32 + lane;                           // row in the tile
+    const uint64_t c2 = pair_of(sh.c, sh.c);
+    Phase sn, on;
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) {      // one decision for the warp
-      if (ok && __any_sync(0xffffffffu, !mbar_wait(bar, parity, wait_cycles))) ok = false;
+    auto wait = [&](uint32_t bar, uint32_t parity) {       // one decision for the warp
+      ok = !__any_sync(0xffffffffu, !mbar_wait(bar, parity, wait_cycles));
       fence_after();
       return ok;
     };
-    auto wait_slot = [&](int g) { return wait(full0 + 8 * (g % kStages), (g / kStages) & 1); };
-    const uint64_t q_desc = sw128_desc(s0), k_desc = sw128_desc(ring), v_desc = sw128_desc(ring, kBox);
-    auto score = [&](int h, int g) {                       // S_h = Q_h K^T
-      if (elect_one()) {
-        const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)((g % kStages) * kTile >> 4);
-        const uint32_t acc = tmem + h * kT;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * kBox + 32 * (ks & 3)) >> 4;
-          mma_ss(acc, qd + off, kd + off, idesc(kT, false), ks > 0);
-        }
-        mma_commit(sfull + 8 * h);
-      }
+    for (uint32_t u = 0;; ++u) {
+      if (!wait(wfull + 8 * (u & 1), (u >> 1) & 1)) break;
+      const Work w = work[u & 1];
       __syncwarp();
-    };
-    auto signal = [&](uint32_t bar) {
-      if (elect_one()) mma_commit(bar);
-      __syncwarp();
-    };
-    if (wait_slot(0)) {
-      for (int h = 0; h < 2; ++h)
-        if (blocks_of(h) && wait(qfull + 8 * h, 0)) score(h, 0);
-      signal(empty0);
-    }
-    const int ragged = len % kT;                           // keys of the sequence's last block (0: all)
-    for (int j = 0; j < nb && ok; ++j) {
-      const int gv = 2 * j + 1, gk = 2 * j + 2;
-      if (!wait_slot(gv)) break;
-      if (ragged && j == len / kT) {
-        // rows of V after the sequence's end: their weights are zero, but
-        // zero times a NaN or an infinity is not
-        for (int x = 0; x < D / 64; ++x)
-          for (int i = ragged * 8 + lane; i < kT * 8; i += 32)
-            *reinterpret_cast<uint4*>(smem + 2 * kTile + (gv % kStages) * kTile + x * kBox + 16 * i) =
-                make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
-      for (int h = 0; h < 2 && ok; ++h) {
-        const int mine = h ? nb1 : nb0;
-        if (j >= mine) continue;
-        const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
-        for (int half = 0; half < 2 && ok; ++half) {
-          if (!wait(pfull + 16 * h + 8 * half, j & 1)) break;
-          if (elect_one()) {
-            const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT + 32 * half;
-            const uint64_t vh = vd + (uint64_t)(2048 * 4 * half >> 4);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_ts(acc, pd + 8 * x, vh + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j + half > 0));
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (j + 1 < mine) {
-          if (!wait_slot(gk)) break;
-          score(h, gk);
-        } else {
-          signal(ofull + 8 * h);
-        }
-      }
-      if (!ok) break;
-      signal(empty0 + 8 * (gv % kStages));
-      if (j + 1 < nb) signal(empty0 + 8 * (gk % kStages));
-    }
-    if (!ok) failed = 1;
-    // never free TMEM under a running MMA
-    signal(mdone);
-    if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
-  } else {
-    const int h = warp >> 2, q = warp & 3;
-    const int mine = h ? nb1 : nb0;
-    const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t ts = tmem + lanes + h * kT, to = tmem + lanes + 2 * kT + h * kT;
-    const int r = q * 32 + lane, row = row_of(h) + r;      // row in the tile and in the sequence
-    float m = -INFINITY;
-    uint64_t l2[2] = {0, 0};                               // the row's sum, in four parts
-    const uint64_t c2 = pair_of(sh.c, sh.c);
-    bool ok = true;
-    for (int j = 0; j < mine && ok; ++j) {
-      if (__any_sync(0xffffffffu, !mbar_wait(sfull + 8 * h, j & 1, wait_cycles))) {
-        ok = false;
-        break;
-      }
-      fence_after();
-      const bool diagonal = j == mine - 1;
-      uint32_t s[4][32];
-      tmem_ld32(ts, s[0]);
-      tmem_ld32(ts + 32, s[1]);
-      tmem_ld_wait();
-      tmem_ld32(ts + 64, s[2]);
-      tmem_ld32(ts + 96, s[3]);
-      if (diagonal) mask64(s[0], s[1], r);
-      float top = max32(s[1], max32(s[0], -INFINITY));
-      tmem_ld_wait();
-      if (diagonal) mask64(s[2], s[3], r - 64);
-      top = max32(s[3], max32(s[2], top));
-      const bool grow = j == 0 || (top - m) * sh.c > kGrow;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mnew = grow ? top : m;
-        if (j > 0) {
-          const float alpha = ex2((m - mnew) * sh.c);      // 1 where the maximum stays
-          const uint64_t a2 = pair_of(alpha, alpha);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) l2[x] = fma2(l2[x], a2, 0);
-#pragma unroll 1
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t o[16];
-            tmem_ld16(to + 16 * i, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(to + 16 * i, o);
-          }
-        }
-        m = mnew;
-      }
-      const float mc = m * sh.c;
-      const uint64_t mc2 = pair_of(-mc, -mc);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      if (lane == 0) mbar_arrive(wempty + 8 * (u & 1));
+      if (!w.len) break;
+      const int mine = w.blocks(sh, h);
+      if (!mine) continue;
+      float m = -INFINITY;
+      uint64_t l2[2] = {0, 0};                             // the row's sum, in four parts
+      for (int j = 0; j < mine; ++j) {
+        if (!wait(sfull + 8 * h, sn.next())) break;
+        const bool diagonal = j == mine - 1;
+        uint32_t s[4][32];
+        tmem_ld32(ts, s[0]);
+        tmem_ld32(ts + 32, s[1]);
+        tmem_ld_wait();
+        tmem_ld32(ts + 64, s[2]);
+        tmem_ld32(ts + 96, s[3]);
+        if (diagonal) mask64(s[0], s[1], r);
+        float top = max32(s[1], max32(s[0], -INFINITY));
+        tmem_ld_wait();
+        if (diagonal) mask64(s[2], s[3], r - 64);
+        top = max32(s[3], max32(s[2], top));
+        // The first half of the weights is formed with the maximum that the
+        // row had before this block, under the search for the block's own;
+        // they are formed again in the rare block that moves the maximum.
         uint32_t p[32];
+        uint64_t sum[2];
+        weights(s[0], s[1], c2, m * sh.c, p, sum);
+        const bool grow = j == 0 || (top - m) * sh.c > kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mnew = grow ? top : m;
+          if (j > 0) {
+            const float alpha = ex2((m - mnew) * sh.c);    // 1 where the maximum stays
+            const uint64_t a2 = pair_of(alpha, alpha);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int i = 64 * half + 2 * e;
-          const float2 x = pair_to(
-              fma2(pair_of(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2, mc2));
-          const float a = ex2(x.x), b = ex2(x.y);
-          l2[e & 1] = add2(l2[e & 1], pair_of(a, b));
-          p[e] = pack_bf16(a, b);
+            for (int x = 0; x < 2; ++x) l2[x] = fma2(l2[x], a2, 0);
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(to + 16 * i, o);
+            }
+          }
+          m = mnew;
+          weights(s[0], s[1], c2, m * sh.c, p, sum);
         }
-        tmem_st32(ts + 32 * half, p);
+        tmem_st32(ts, p);
+        l2[0] = add2(l2[0], sum[0]);
+        l2[1] = add2(l2[1], sum[1]);
         tmem_st_wait();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull + 16 * h + 8 * half);
+        if (lane == 0) mbar_arrive(pfull + 16 * h);
+        weights(s[2], s[3], c2, m * sh.c, p, sum);
+        tmem_st32(ts + 32, p);
+        l2[0] = add2(l2[0], sum[0]);
+        l2[1] = add2(l2[1], sum[1]);
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + 16 * h + 8);
       }
-    }
-    const float2 la = pair_to(l2[0]), lb = pair_to(l2[1]);
-    const float l = (la.x + la.y) + (lb.x + lb.y);
-    if (mine && ok && __any_sync(0xffffffffu, !mbar_wait(ofull + 8 * h, 0, wait_cycles))) ok = false;
-    if (!ok) failed = 1;
-    if (mine && ok) {
-      fence_after();
-      const float inv = 1.f / l;
+      if (!ok || !wait(ofull + 8 * h, on.next())) break;
+      const float2 la = pair_to(l2[0]), lb = pair_to(l2[1]);
+      const float inv = 1.f / ((la.x + la.y) + (lb.x + lb.y));
+      const int row = w.row(sh, h) + r;
       bool bad = false;
-      uint16_t* op = O + (long long)(first + row) * sh.ldo + head_of(h) * D;
+      uint16_t* op = O + (long long)(w.first + row) * sh.ldo + w.head(sh, h) * D;
 #pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         uint32_t o[32];
@@ -422,14 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           bad |= !(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY);
           v[e] = pack_bf16(a, b);
         }
-        if (row < len) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(op + 32 * i + 8 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        if (row < w.len) {
+          store32(op + 32 * i, v, sh.wide);
+          store32(op + 32 * i + 16, v + 8, sh.wide);
         }
       }
-      if (bad && row < len) set_info(info, SGPT_INFO_NONFINITE);
+      fence_before();                                      // O is read: the next unit's weights follow
+      if (bad && row < w.len) set_info(info, SGPT_INFO_NONFINITE);
     }
+    if (!ok) failed = 1;
   }
   fence_before();
   __syncthreads();
@@ -459,9 +600,8 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
     return cudaFuncSetAttribute(attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_for(D));
   });
   if (e != cudaSuccess) return e;
-  attention_kernel<D><<<(unsigned)ctas, kThreads, smem_for(D), st>>>(qm, km, vm, cu, sh, O, info, wait_limit_cycles());
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_after(attention_kernel<D>, (unsigned)ctas, kThreads, smem_for(D), 1, st, qm, km, vm, cu, sh, O, info,
+                      wait_limit_cycles());
 }
 
 }  // namespace
@@ -488,6 +628,7 @@ cudaError_t launch_attention(const uint16_t* Q, long long ldq, const uint16_t* K
   sh.heads = heads;
   sh.group = heads / kv_heads;
   sh.pair = sh.group % 2 == 0;
+  sh.wide = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 && ldo % 16 == 0;
   sh.c = (float)((double)scale * 1.4426950408889634);
   const long long ctas = attention_ctas(n_tok, n_seq, heads, kv_heads);
   return D == 128 ? launch<128>(qm, km, vm, cu, sh, ctas, O, info, st)

@@ -177,6 +177,30 @@ __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y
                : "memory");
 }
 
+// ---------------------------------------------------------- grid as a queue
+//
+// Asks for the index of a CTA of this grid that has not started yet: the
+// answer (16 bytes at `answer`, completing on `bar`) names it, and it then
+// never starts. After an answer that names none, no further request is made.
+__device__ __forceinline__ void steal_cta(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+// The index (x) that an answer names, or -1.
+__device__ __forceinline__ int stolen_cta(uint32_t answer) {
+  uint32_t x = 0, ok = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 a;\n ld.shared.b128 a, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %1, 1, 0, p;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, a;\n}\n"
+      : "+r"(x), "=r"(ok)
+      : "r"(answer)
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
 // --------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
