@@ -367,19 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     } else if (warp == 9) {
       if (elect_one()) {
         const uint64_t q_desc = sw128_desc(s0), k_desc = sw128_desc(ring), v_desc = sw128_desc(ring, kBox);
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, wait_cycles)) ok = false;
-          fence_after();
-          return ok;
-        };
-        uint32_t g = 0, groups = 0;
-        Phase qn[2], pn[2], vn;
-        auto wait_slot = [&](uint32_t x) { return wait(full0 + 8 * (x % kStages), (x / kStages) & 1); };
-        auto free_group = [&] {
-          mma_commit(free0 + 8 * (groups % kFree));
-          ++groups;
-        };
+        // No instruction more than needed between the products: the tensor
+        // cores idle while this thread is late.
+        auto loaded = [&](uint32_t x) { return mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, wait_cycles); };
         auto score = [&](int h, uint32_t x, bool last) {   // S_h = Q_h K^T
           const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)((x % kStages) * kTile >> 4);
           const uint32_t acc = tmem + h * kT;
@@ -391,49 +381,58 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           mma_commit(sfull + 8 * h);
           if (last) mma_commit(qempty + 8 * h);
         };
-        for (uint32_t u = 0; ok; ++u) {
-          if (!wait(wfull + 8 * (u & 1), (u >> 1) & 1)) break;
-          const Work w = work[u & 1];
-          mbar_arrive(wempty + 8 * (u & 1));
-          if (!w.len) break;
-          const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
-          if (!wait_slot(g)) break;
-          for (int h = 0; h < 2; ++h)
-            if ((h ? nb1 : nb0) && wait(qfull + 8 * h, qn[h].next())) score(h, g, (h ? nb1 : nb0) == 1);
-          if (!ok) break;
-          free_group();
-          for (int j = 0; j < nb; ++j) {
-            const uint32_t gv = g + 2 * j + 1, gk = gv + 1;
-            if (!wait_slot(gv)) break;
-            if (j == w.len / kT) {                         // the sequence ends inside this block
-              mbar_arrive(vask);
-              if (!wait(vready, vn.next())) break;
-            }
-            const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
+        auto units_done = [&]() -> bool {                  // false: a wait ran out
+          uint32_t g = 0, groups = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, vn = 0;
+          for (uint32_t u = 0;; ++u) {
+            if (!mbar_wait(wfull + 8 * (u & 1), (u >> 1) & 1, wait_cycles)) return false;
+            const Work w = work[u & 1];
+            mbar_arrive(wempty + 8 * (u & 1));
+            if (!w.len) return true;
+            const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
+            const int tail = w.len % kT ? w.len / kT : nb; // the block inside which the sequence ends
+            if (!loaded(g)) return false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int mine = h ? nb1 : nb0;
-              if (j >= mine || !ok) continue;
-              const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT, par = pn[h].next();
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (!wait(pfull + 16 * h + 8 * half, par)) break;
-#pragma unroll
-                for (int x = 4 * half; x < 4 * half + 4; ++x)
-                  mma_ts(acc, pd + 8 * x, vd + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j > 0));
-              }
-              if (j + 1 < mine) {
-                if (wait_slot(gk)) score(h, gk, j + 2 == mine);
-              } else {
-                mma_commit(ofull + 8 * h);
-              }
+              if (!mine) continue;
+              if (!mbar_wait(qfull + 8 * h, qn[h]++ & 1, wait_cycles)) return false;
+              score(h, g, mine == 1);
             }
-            if (!ok) break;
-            free_group();
+            mma_commit(free0 + 8 * (groups++ % kFree));
+            for (int j = 0; j < nb; ++j) {
+              const uint32_t gv = ++g;
+              if (!loaded(gv)) return false;
+              if (j == tail) {
+                mbar_arrive(vask);
+                if (!mbar_wait(vready, vn++ & 1, wait_cycles)) return false;
+              }
+              const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
+              ++g;                                         // the next block's K
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int mine = h ? nb1 : nb0;
+                if (j >= mine) continue;
+                const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT, par = pn[h]++ & 1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  if (!mbar_wait(pfull + 16 * h + 8 * half, par, wait_cycles)) return false;
+                  fence_after();
+#pragma unroll
+                  for (int x = 4 * half; x < 4 * half + 4; ++x)
+                    mma_ts(acc, pd + 8 * x, vd + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j > 0));
+                }
+                if (j + 1 < mine) {
+                  if (!loaded(g)) return false;
+                  score(h, g, j + 2 == mine);
+                } else {
+                  mma_commit(ofull + 8 * h);
+                }
+              }
+              mma_commit(free0 + 8 * (groups++ % kFree));
+            }
           }
-          g += 2 * nb;
-        }
-        if (!ok) failed = 1;
+        };
+        if (!units_done()) failed = 1;
         // never free TMEM under a running MMA
         mma_commit(mdone);
         if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
@@ -548,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const float2 la = pair_to(l2[0]), lb = pair_to(l2[1]);
       const float inv = 1.f / ((la.x + la.y) + (lb.x + lb.y));
       const int row = w.row(sh, h) + r;
-      bool bad = false;
+      uint64_t bad = 0;                                    // a sum of o * 0: NaN if one is not finite
+      const uint64_t inv2 = pair_of(inv, inv);
       uint16_t* op = O + (long long)(w.first + row) * sh.ldo + w.head(sh, h) * D;
 #pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
@@ -558,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
-          bad |= !(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY);
-          v[e] = pack_bf16(a, b);
+          const uint64_t y = fma2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2, 0);
+          bad = fma2(y, 0, bad);
+          v[e] = pack_bf16(pair_to(y).x, pair_to(y).y);
         }
         if (row < w.len) {
           store32(op + 32 * i, v, sh.wide);
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
       }
       fence_before();                                      // O is read: the next unit's weights follow
-      if (bad && row < w.len) set_info(info, SGPT_INFO_NONFINITE);
+      if (!(pair_to(bad).x + pair_to(bad).y == 0.f) && row < w.len) set_info(info, SGPT_INFO_NONFINITE);
     }
     if (!ok) failed = 1;
   }

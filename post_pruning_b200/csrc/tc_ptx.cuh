@@ -50,16 +50,12 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 }
 // Bounded wait: false when `limit` SM cycles passed before the phase ended
 // (short limits poll without suspending the thread, so they run out at once).
+// A phase that has ended costs one test.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long limit) {
-  if (limit < kShortWaitCycles) {
-    const long long t0 = clock64();
-    while (!mbar_test(bar, parity))
-      if (clock64() - t0 > limit) return false;
-    return true;
-  }
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try(bar, parity))
+  const bool poll = limit < kShortWaitCycles;
+  while (!(poll ? mbar_test(bar, parity) : mbar_try(bar, parity)))
     if (clock64() - t0 > limit) return false;
   return true;
 }
