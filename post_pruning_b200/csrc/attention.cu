@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
+  let_next_start();
   after_previous();
   if (cta_info_set(info)) return;
   if (blockIdx.x == 0) {                         // every offset is checked once

@@ -96,19 +96,95 @@ __device__ __forceinline__ Channel channel(const Out& o, int row) {
   return c;
 }
 
+constexpr int kMaxSplit = 8;                    // parts of K at most
+constexpr int kAhead = 8;                       // stages of codes fetched into the L2 before the predecessor has ended
+
+// y of one token and channel from the exact sum of products.
+__device__ __forceinline__ float result(int sum, const Channel& ch, float tok_scale, int tok_sum) {
+  return (float)(sum - ch.zero * tok_sum) * ch.scale * tok_scale;
+}
+
+// Four consecutive channels of a token.
+__device__ __forceinline__ void store4(float* y, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(uint16_t* y, const float (&v)[4]) {
+  ushort4 o;
+  store_y(&o.x, v[0]);
+  store_y(&o.y, v[1]);
+  store_y(&o.z, v[2]);
+  store_y(&o.w, v[3]);
+  *reinterpret_cast<ushort4*>(y) = o;
+}
+
+// The split sums: every CTA of the cluster holds its part of a tile, token by
+// token, at `part` ([tokens][128] int32); this one's epilogue warps (w of 4)
+// add up and write every `split`-th token. first + step * p: the CTA of part
+// p. A lane takes four channels: 16 bytes of distributed shared memory at a
+// time, 16 loads in flight, are what keeps this short.
+template <class T>
+__device__ __forceinline__ void add_parts(uint32_t part, int split, int sp, int first, int step, int w, int lane,
+                                          int row0, int n0, int cols, const Out& out, const float* tok_scale,
+                                          const int32_t* tok_sum) {
+  const int rows = out.rows, row = row0 + 4 * lane;
+  Channel ch[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) ch[x] = channel(out, row + x);
+  const bool whole = rows % 4 == 0 && row + 3 < rows;
+  T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
+  const int every = 4 * split;
+  for (int c0 = sp + split * w; c0 < cols; c0 += 4 * every) {
+    int4 acc[4] = {};
+#pragma unroll 4
+    for (int p = 0; p < split; ++p) {
+      const uint32_t from = map_rank(part + 16 * lane, first + step * p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * every;
+        if (c >= cols) continue;
+        const int4 v = ld_cluster4(from + 4 * kBM * c);
+        acc[i].x += v.x;
+        acc[i].y += v.y;
+        acc[i].z += v.z;
+        acc[i].w += v.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * every;
+      if (c >= cols) continue;
+      const int sum[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
+      float v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = result(sum[x], ch[x], tok_scale[c], tok_sum[c]);
+      T* y = Y + (long long)c * rows;
+      if (whole) {
+        store4(y, v);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (row + x < rows) store_y(y + x, v[x]);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ CTA pairs
 
-constexpr int kPairN = 256;                     // tokens per tile
-constexpr int kPairStages = 6;
-constexpr int kPairStage = 2 * kABytes;         // per CTA: 128 channels and 128 tokens
-constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + 1024 + 256 + 2 * 8 * kPairN;
+__host__ __device__ constexpr int pair_stage(int bn) { return kABytes + bn / 2 * kBK; }   // per CTA
+__host__ __device__ constexpr int pair_stages(int bn) { return bn > 128 ? 6 : 8; }
+__host__ __device__ constexpr size_t pair_smem(int bn) {
+  return (size_t)pair_stages(bn) * pair_stage(bn) + 1024 + 256 + 2 * 8 * bn;
+}
 constexpr int kGroupRows = 8;                   // 256-channel tile rows walked together
 
-template <class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(
-    const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, int d, const Out out, int* info,
-    const long long wait_cycles) {
-  constexpr int kStages = kPairStages, kStage = kPairStage, BN = kPairN;
+template <int BN, class T>
+__global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                     const __grid_constant__ CUtensorMap xmap, int d,
+                                                                     int split, const Out out, int* info,
+                                                                     const long long wait_cycles) {
+  constexpr int kStages = pair_stages(BN), kStage = pair_stage(BN);
+  static_assert(BN * kBM * 4 <= kStages * kStage, "the parts of a split sum fit the ring");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // both CTAs lay their shared memory out alike: the pair's barriers and
   // operands are addressed by the same offsets
@@ -119,40 +195,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
   int32_t* tok_sum = reinterpret_cast<int32_t*>(tok_scale + 2 * BN);                // [2][BN]
   __shared__ uint32_t tmem_slot;
   __shared__ int failed, skip;
+  let_next_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = cluster_rank(), leader = rank & ~1u, half = rank & 1u;   // the pair's first CTA; this one's half
+  const int sp = (int)(rank >> 1);                           // this pair's part of K
+  const uint16_t both = (uint16_t)(3u << leader);
   const int rows = out.rows, n = out.n;
   const int mt_count = cdiv(rows, 2 * kBM), nt_count = cdiv(n, BN), kt_count = cdiv(d, kBK);
+  const int k0 = (int)((long long)kt_count * sp / split), k1 = (int)((long long)kt_count * (sp + 1) / split);
   const long long items = (long long)mt_count * nt_count;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int first_item = blockIdx.x / (2 * split), step = gridDim.x / (2 * split);
   const uint32_t s0 = smem_u32(smem);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, mdone = tempty0 + 16;
-  if (threadIdx.x == 0) {
-    prefetch_map(&wmap);
-    prefetch_map(&xmap);
-    failed = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);              // used in the first CTA
-      mbar_init(empty0 + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 8);            // used in the first CTA: four warps of each
-    }
-    mbar_init(mdone, 1);
-    mbar_init_fence();
-  }
-  if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
-  after_previous();
-  if (threadIdx.x == 0) skip = info_set(info);
-  fence_before();
-  cluster_sync();
-  fence_after();
-  const uint32_t tmem = tmem_slot;
-  // one decision for the pair: the first CTA's look at *info
-  const bool run = ld_cluster(map_rank(smem_u32(&skip), 0)) == 0;
-
   auto decode = [&](long long w, int& mt, int& nt) {
     const long long per_group = (long long)kGroupRows * nt_count;
     const int g = (int)(w / per_group);
@@ -162,70 +217,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
     mt = first + (int)(r % grows);
     nt = (int)(r / grows);
   };
+  if (threadIdx.x == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    failed = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);              // used in the pair's first CTA
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 8);            // used in the pair's first CTA: four warps of each
+    }
+    mbar_init(mdone, 1);
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
+  if (warp == 1 && lane == 0) {
+    int mt, nt;
+    decode(first_item, mt, nt);
+    for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * 2 * kBM + (int)half * kBM);
+  }
+  after_previous();
+  if (threadIdx.x == 0) skip = info_set(info);
+  fence_before();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  // one decision for the cluster: its first CTA's look at *info
+  const bool run = ld_cluster(map_rank(smem_u32(&skip), 0)) == 0;
 
   if (warp == 0) {
-    if (lane == 0 && run) {
-      const uint32_t leader_full0 = map_rank(full0, 0);
+    if (run && elect_one()) {
+      const uint32_t leader_full0 = map_rank(full0, leader);
       long long g = 0;
-      for (long long w = pair; w < items && !failed; w += pairs) {
+      for (long long w = first_item; w < items && !failed; w += step) {
         int mt, nt;
         decode(w, mt, nt);
-        for (int i = 0; i < kt_count; ++i, ++g) {
+        for (int i = k0; i < k1; ++i, ++g) {
           const int s = (int)(g % kStages);
           if (g >= kStages && !mbar_wait(empty0 + 8 * s, (uint32_t)((g / kStages) & 1) ^ 1, wait_cycles)) {
             failed = 1;
             break;
           }
           const uint32_t bar = leader_full0 + 8 * s, sa = s0 + s * kStage;
-          if (rank == 0) mbar_expect(full0 + 8 * s, 2 * kStage);      // both CTAs' copies
-          tma_2d_pair(sa, &wmap, bar, i * kBK, mt * 2 * kBM + (int)rank * kBM);
-          tma_2d_pair(sa + kABytes, &xmap, bar, i * kBK, nt * BN + (int)rank * (BN / 2));
+          if (half == 0) mbar_expect(full0 + 8 * s, 2 * kStage);      // both CTAs' copies
+          tma_2d_pair(sa, &wmap, bar, i * kBK, mt * 2 * kBM + (int)half * kBM);
+          tma_2d_pair(sa + kABytes, &xmap, bar, i * kBK, nt * BN + (int)half * (BN / 2));
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0 && run) {
+    if (half == 0 && run && elect_one()) {
+      const uint64_t a_desc = sw128_desc(s0), b_desc = sw128_desc(s0 + kABytes);
       long long g = 0;
       int u = 0;
-      for (long long w = pair; w < items && !failed; w += pairs, ++u) {
+      for (long long w = first_item; w < items && !failed; w += step, ++u) {
         const int b = u & 1;
         if (u >= 2 && !mbar_wait(tempty0 + 8 * b, ((u >> 1) & 1) ^ 1, wait_cycles)) {
           failed = 1;
           break;
         }
         fence_after();
-        for (int i = 0; i < kt_count; ++i, ++g) {
+        for (int i = k0; i < k1; ++i, ++g) {
           const int s = (int)(g % kStages);
           if (!mbar_wait(full0 + 8 * s, (uint32_t)(g / kStages) & 1, wait_cycles)) {
             failed = 1;
             break;
           }
           fence_after();
-          const uint32_t sa = s0 + s * kStage;
+          const uint64_t off = (uint64_t)(s * kStage >> 4);
 #pragma unroll
           for (int j = 0; j < kBK / 32; ++j)
-            mma_i8<1>(tmem + b * BN, sw128_desc(sa + 32 * j), sw128_desc(sa + kABytes + 32 * j), idesc(2 * kBM, BN),
-                      (i > 0 || j > 0) ? 1u : 0u);
-          mma_commit2(empty0 + 8 * s);
+            mma_i8<1>(tmem + b * BN, a_desc + off + 2 * j, b_desc + off + 2 * j, idesc(2 * kBM, BN),
+                      j > 0 ? 1u : (uint32_t)(i > k0));
+          mma_commit2(empty0 + 8 * s, both);
         }
         if (failed) break;
-        mma_commit2(tfull0 + 8 * b);
+        mma_commit2(tfull0 + 8 * b, both);
       }
       // never free TMEM under a running MMA
-      mma_commit2(mdone);
+      mma_commit2(mdone, both);
       if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
     }
   } else if (run) {
     const int q = warp & 3, et = threadIdx.x - 64;       // TMEM lanes 32 q .. of this warp; epilogue thread
-    const uint32_t leader_tempty0 = map_rank(tempty0, 0);
-    T* Y = static_cast<T*>(out.Y);
+    const uint32_t leader_tempty0 = map_rank(tempty0, leader);
     int u = 0;
-    for (long long w = pair; w < items; w += pairs, ++u) {
+    for (long long w = first_item; w < items; w += step, ++u) {
       int mt, nt;
       decode(w, mt, nt);
-      const int b = u & 1, n0 = nt * BN, row = mt * 2 * kBM + (int)rank * kBM + q * 32 + lane;
+      const int b = u & 1, n0 = nt * BN, row = mt * 2 * kBM + (int)half * kBM + q * 32 + lane;
+      const int cols = min(BN, n - n0);
       for (int e = et; e < BN; e += 128) {
-        const bool in = n0 + e < n;
+        const bool in = e < cols;
         tok_scale[b * BN + e] = in ? out.xs[n0 + e] : 0.f;
         tok_sum[b * BN + e] = in ? out.xsum[n0 + e] : 0;
       }
@@ -237,18 +322,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       if (bad) failed = 1;
       fence_after();
       if (!bad) {
-        const int cols = min(BN, n - n0);
-        T* yp = Y + (long long)n0 * rows + row;
+        T* yp = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
+        int32_t* part = reinterpret_cast<int32_t*>(smem) + q * 32 + lane;
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
           uint32_t v[32];
           tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + c), v);
           tmem_ld_wait();
-          if (row < rows) {
+          if (split > 1) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) part[(c + e) * kBM] = (int32_t)v[e];
+          } else if (row < rows) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const int acc = (int)v[e] - ch.zero * tok_sum[b * BN + c + e];
-              if (c + e < cols) store_y(yp, (float)acc * ch.scale * tok_scale[b * BN + c + e]);
+              if (c + e < cols) store_y(yp, result((int)v[e], ch, tok_scale[b * BN + c + e], tok_sum[b * BN + c + e]));
               yp += rows;
             }
           }
@@ -258,6 +345,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * b);
       // a warp that gave up still meets the others at the named barrier of the remaining tiles
+    }
+  }
+  if (split > 1) {                              // one tile per cluster
+    cluster_sync();
+    bool all = run;
+    for (int p = 0; p < 2 * split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
+    if (warp >= 2 && all) {
+      int mt, nt;
+      decode(first_item, mt, nt);
+      add_parts<T>(s0, split, sp, (int)half, 2, warp - 2, lane, mt * 2 * kBM + (int)half * kBM, nt * BN,
+                   min(BN, n - nt * BN), out, tok_scale, tok_sum);
     }
   }
   __syncwarp();
@@ -271,30 +369,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
     }
   }
   __syncthreads();
-  cluster_sync();                               // the pair ends together: MMAs and barriers reach into both CTAs
+  cluster_sync();                               // the cluster ends together: MMAs, barriers and sums reach into its CTAs
   if (warp == 0) tmem_free2(tmem, 2 * BN);
 }
 
 // ---------------------------------------------------- one tile, split over K
 
-constexpr int kMaxSplit = 8;                    // CTAs of a cluster that share a tile
-constexpr int kAhead = 8;                       // stages of codes fetched into the L2 before the predecessor has ended
 
-__host__ __device__ constexpr int split_stages(int bn) { return bn <= 64 ? 4 : 3; }
+constexpr int kSplitStages = 4;
 __host__ __device__ constexpr int split_stage(int bn) { return kABytes + bn * kBK; }
 __host__ __device__ constexpr size_t split_smem(int bn) {
-  return (size_t)split_stages(bn) * split_stage(bn) + 1024 + 128;
+  return (size_t)kSplitStages * split_stage(bn) + 1024 + 128;
 }
 // CTAs that fit on an SM together
 __host__ __device__ constexpr int split_per_sm(int bn) { return bn <= 16 ? 3 : 2; }
-static_assert(3 * (split_smem(16) + 1280) <= 233472 && 2 * (split_smem(128) + 2176) <= 233472, "CTAs per SM");
+static_assert(3 * (split_smem(16) + 1280) <= 233472 && 2 * (split_smem(64) + 1664) <= 233472, "CTAs per SM");
 
 template <int BN, class T>
 __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                    const __grid_constant__ CUtensorMap xmap, int d,
                                                                    int split, const Out out, int* info,
                                                                    const long long wait_cycles) {
-  constexpr int kStages = split_stages(BN), kStage = split_stage(BN);
+  constexpr int kStages = kSplitStages, kStage = split_stage(BN);
   constexpr uint32_t kCols = BN < 32 ? 32 : BN;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -304,6 +400,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   __shared__ int failed, skip;
   __shared__ float tok_scale[BN];
   __shared__ int32_t tok_sum[BN];
+  let_next_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();                    // this CTA's part of K
   const int tile = blockIdx.x / split;
@@ -404,10 +501,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
         tmem_ld_wait();
         if (row >= rows) continue;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float y = (float)((int)v[e] - ch.zero * tok_sum[c + e]) * ch.scale * tok_scale[c + e];
-          if (c + e < cols) store_y(Y + (long long)(c + e) * rows, y);
-        }
+        for (int e = 0; e < 16; ++e)
+          if (c + e < cols) store_y(Y + (long long)(c + e) * rows, result((int)v[e], ch, tok_scale[c + e], tok_sum[c + e]));
       }
     }
   } else {
@@ -429,17 +524,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     bool all = true;
     for (int p = 0; p < split; ++p)
       all = all && (ld_cluster(map_rank(smem_u32(&failed), p)) | ld_cluster(map_rank(smem_u32(&skip), p))) == 0;
-    if (warp >= 2 && all && row < rows) {
-      const uint32_t mine = s0 + 4 * r;
-#pragma unroll 2
-      for (int c = rank; c < cols; c += split) {
-        int acc = 0;
-#pragma unroll
-        for (int p = 0; p < kMaxSplit; ++p)
-          if (p < split) acc += ld_cluster(map_rank(mine + 4 * kBM * c, p));
-        store_y(Y + (long long)c * rows, (float)(acc - ch.zero * tok_sum[c]) * ch.scale * tok_scale[c]);
-      }
-    }
+    if (warp >= 2 && all) add_parts<T>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, tok_scale, tok_sum);
     cluster_sync();                                        // no CTA leaves while its sums are read
   }
   fence_before();
@@ -470,20 +555,34 @@ struct Args {
   cudaStream_t st;
 };
 
-template <class T>
-cudaError_t launch_pair(const Args& a) {
+// What the pair kernel takes on tiles of 256 channels x bn tokens with K in
+// `split` parts, in twentieths of a 256 x 256 tile's K stage (about 16 ns):
+// waves of 74 pairs, each of kt / split stages (a stage of a 256 x 128 tile
+// measured 0.7 of a 256 x 256 tile's: 225 and 325 ns), and the adding of the
+// parts (2 to 3 us at bn = 256). K in more than two is not tried: clusters
+// of eight such CTAs do not all find room at once (16 of them took two waves).
+long long pair_cost(int rows, int n, int d, int bn, int split) {
+  const long long items = (long long)cdiv(rows, 2 * kBM) * cdiv(n, bn);
+  const int kt = cdiv(d, kBK), pairs = kNumSMs / 2;
+  if (split > 1 && (items * split > pairs || split > kt)) return INT64_MAX;
+  return cdivll(items * split, pairs) * cdiv(kt, split) * (bn > 128 ? 20 : 14) + (split > 1 ? bn * 2 / 3 : 0);
+}
+
+template <int BN, class T>
+cudaError_t launch_pair(const Args& a, int split) {
   CUtensorMap wm, xm;
-  if (!map_i8(&wm, a.codes, a.out.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.out.n, a.d, kPairN / 2))
+  if (!map_i8(&wm, a.codes, a.out.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.out.n, a.d, BN / 2))
     return cudaErrorInvalidValue;
   static PerDevice attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(linear_i8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    return cudaFuncSetAttribute(linear_i8_pair_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)pair_smem(BN));
   });
   if (e != cudaSuccess) return e;
-  const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, kPairN);
-  const int pairs = (int)std::min<long long>(items, kNumSMs / 2);
-  return launch_after(linear_i8_pair_kernel<T>, 2 * pairs, kThreads, kPairSmem, 1, a.st, wm, xm, a.d, a.out, a.info,
-                      wait_limit_cycles());
+  const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, BN);
+  const int pairs = split > 1 ? (int)items * split : (int)std::min<long long>(items, kNumSMs / 2);
+  return launch_after(linear_i8_pair_kernel<BN, T>, 2 * pairs, kThreads, pair_smem(BN), 2 * split, a.st, wm, xm, a.d,
+                      split, a.out, a.info, wait_limit_cycles());
 }
 
 template <int BN, class T>
@@ -507,13 +606,22 @@ cudaError_t launch_split(const Args& a) {
 
 template <class T>
 cudaError_t dispatch(const Args& a) {
-  const long long n = a.out.n, pair_tiles = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, kPairN);
+  const int n = a.out.n;
   if (n <= 16) return launch_split<16, T>(a);
   if (n <= 32) return launch_split<32, T>(a);
   if (n <= 64) return launch_split<64, T>(a);
-  if (pair_tiles >= kNumSMs / 4) return launch_pair<T>(a);
-  if ((long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, 128) < kNumSMs) return launch_split<64, T>(a);
-  return launch_split<128, T>(a);
+  long long best = INT64_MAX;
+  int bn = 128, split = 1;
+  for (const int b : {256, 128})
+    for (const int p : {1, 2}) {
+      const long long c = pair_cost(a.out.rows, n, a.d, b, p);
+      if ((b == 128 || n > 128) && c < best) {
+        best = c;
+        bn = b;
+        split = p;
+      }
+    }
+  return bn == 256 ? launch_pair<256, T>(a, split) : launch_pair<128, T>(a, split);
 }
 
 }  // namespace

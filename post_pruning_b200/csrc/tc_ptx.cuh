@@ -221,6 +221,14 @@ __device__ __forceinline__ int32_t ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void add_cluster(uint32_t addr, int32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -237,12 +245,12 @@ __device__ __forceinline__ void tmem_alloc2(uint32_t slot, uint32_t cols) {
 __device__ __forceinline__ void tmem_free2(uint32_t tmem, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
 }
-// Arrives at this offset's barrier in both CTAs of the pair when the MMAs
-// issued so far are done.
-__device__ __forceinline__ void mma_commit2(uint32_t bar) {
+// Arrives at this offset's barrier in the cluster's CTAs of `mask` (both of
+// the pair) when the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit2(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 // Into this CTA's shared memory; `bar` may be the pair's other CTA's (an

@@ -174,16 +174,21 @@ def _dev(t: torch.Tensor, dtype, name: str):
 
 
 def _one_device(*tensors: torch.Tensor) -> int:
-    """The index of the device of `tensors`, which must be one."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
+    """The index of the CUDA device of `tensors`, which must be one."""
+    try:
+        dev = tensors[0].get_device()                  # -1 on the CPU
+        for t in tensors:
+            if t.get_device() != dev:
+                raise ValueError("all tensors must be on one device")
+    except AttributeError:
+        raise TypeError("all operands must be CUDA tensors") from None
+    if dev < 0:
+        raise TypeError("all operands must be CUDA tensors")
     return dev
 
 
 # the handle of a device's current stream, without the Stream object that
-# torch.cuda.current_stream() builds (3 us of a 10 us call)
+# torch.cuda.current_stream() builds (3 us of a call that takes 6)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -194,7 +199,9 @@ def _enqueue(entry: str, dev: int, stream, *args):
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _enqueue(entry, dev, stream, *args)
-    _check(getattr(lib(), entry)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream), entry)
+    status = getattr(_lib or lib(), entry)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status != SGPT_OK:
+        raise SgptError(status, entry)
 
 
 def _rowmajor(t: torch.Tensor, name: str) -> int:
@@ -447,41 +454,46 @@ def quant_codes(W: torch.Tensor, grid: torch.Tensor, codes: torch.Tensor, dev_in
              _ptr(codes), _ptr(dev_info))
 
 
-def _token_outputs(n: int, d: int, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor):
-    _dev(Xq, torch.int8, "Xq")
-    _dev(scale, torch.float32, "scale")
-    _dev(sums, torch.int32, "sums")
-    if Xq.shape != (n, d) or scale.shape != (n,) or sums.shape != (n,):
-        raise ValueError("Xq must be [n, d], scale and sums [n]")
-    if not (Xq.is_contiguous() and scale.is_contiguous() and sums.is_contiguous()):
-        raise ValueError("Xq, scale and sums must be contiguous")
+# The checks of the calls below are written for a call that takes a few
+# microseconds in all: one expression for the types, one for the shapes.
+
+def _token_codes(n: int, d: int, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor):
+    """Xq [n, d] int8, scale [n] fp32, sums [n] int32, contiguous."""
+    if not (Xq.dtype is torch.int8 and scale.dtype is torch.float32 and sums.dtype is torch.int32):
+        raise TypeError("Xq must be int8, scale float32 and sums int32")
+    if not (Xq.shape == (n, d) and scale.shape == (n,) and sums.shape == (n,) and Xq.is_contiguous()
+            and scale.is_contiguous() and sums.is_contiguous()):
+        raise ValueError("Xq must be [n, d], scale and sums [n], all contiguous")
 
 
 def quant_tokens(X: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor,
                  dev_info: torch.Tensor, stream=None):
     """X [n, d] bf16 to 8 bits with a scale per token (sgpt_quant_tokens):
     Xq [n, d] int8, scale [n] fp32, sums [n] int32 (the codes' row sums)."""
-    _dev(X, torch.bfloat16, "X")
+    dev = _one_device(X, Xq, scale, sums, dev_info)
+    if X.dtype is not torch.bfloat16:
+        raise TypeError("X must be bfloat16")
     ldx = _row_stride(X, "X")
     n, d = X.shape
-    _token_outputs(n, d, Xq, scale, sums)
-    _enqueue("sgpt_quant_tokens", _one_device(X, Xq, scale, sums, dev_info), stream, _ptr(X), n, d, ldx, _ptr(Xq),
-             _ptr(scale), _ptr(sums), _ptr(dev_info))
+    _token_codes(n, d, Xq, scale, sums)
+    _enqueue("sgpt_quant_tokens", dev, stream, X.data_ptr(), n, d, ldx, Xq.data_ptr(), scale.data_ptr(),
+             sums.data_ptr(), dev_info.data_ptr())
 
 
 def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor,
                       dev_info: torch.Tensor, stream=None):
     """quant_tokens of silu(G) * U, an MLP's gated activation, without
     rounding it to bf16 in between (sgpt_quant_tokens_silu)."""
-    _dev(G, torch.bfloat16, "G")
-    _dev(U, torch.bfloat16, "U")
+    dev = _one_device(G, U, Xq, scale, sums, dev_info)
+    if not (G.dtype is torch.bfloat16 and U.dtype is torch.bfloat16):
+        raise TypeError("G and U must be bfloat16")
     ldg, ldu = _row_stride(G, "G"), _row_stride(U, "U")
     n, d = G.shape
     if U.shape != (n, d):
         raise ValueError("G and U must have the same shape")
-    _token_outputs(n, d, Xq, scale, sums)
-    _enqueue("sgpt_quant_tokens_silu", _one_device(G, U, Xq, scale, sums, dev_info), stream, _ptr(G), _ptr(U), n, d, ldg,
-             ldu, _ptr(Xq), _ptr(scale), _ptr(sums), _ptr(dev_info))
+    _token_codes(n, d, Xq, scale, sums)
+    _enqueue("sgpt_quant_tokens_silu", dev, stream, G.data_ptr(), U.data_ptr(), n, d, ldg, ldu, Xq.data_ptr(),
+             scale.data_ptr(), sums.data_ptr(), dev_info.data_ptr())
 
 
 def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: torch.Tensor, grid: torch.Tensor,
@@ -489,29 +501,30 @@ def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: 
     """Y = X W^T in 8-bit integers (sgpt_linear_i8): Xq, scale, sums from
     quant_tokens, codes [d_out, d_in] int8 from quant_codes with its grid and
     qbits, Y [n, d_out] fp32 or bf16."""
-    _dev(codes, torch.int8, "codes")
-    _dev(grid, torch.float32, "grid")
+    dev = _one_device(Xq, scale, sums, codes, grid, Y, dev_info)
+    y_bf16 = Y.dtype is torch.bfloat16
+    if not (codes.dtype is torch.int8 and grid.dtype is torch.float32 and (y_bf16 or Y.dtype is torch.float32)):
+        raise TypeError("codes must be int8, grid float32 and Y float32 or bfloat16")
     if Xq.dim() != 2 or codes.dim() != 2:
         raise ValueError("Xq must be [n, d_in] and codes [d_out, d_in]")
     n, d_in = Xq.shape
     d_out = codes.shape[0]
-    _token_outputs(n, d_in, Xq, scale, sums)
-    y_bf16 = Y.dtype == torch.bfloat16
-    _dev(Y, torch.bfloat16 if y_bf16 else torch.float32, "Y")
-    if codes.shape[1] != d_in or grid.shape != (d_out, 2) or Y.shape != (n, d_out):
-        raise ValueError("codes must be [d_out, d_in], grid [d_out, 2] and Y [n, d_out]")
-    if not (codes.is_contiguous() and grid.is_contiguous() and Y.is_contiguous()):
-        raise ValueError("codes, grid and Y must be contiguous")
-    _enqueue("sgpt_linear_i8", _one_device(Xq, scale, sums, codes, grid, Y, dev_info), stream, _ptr(Xq), _ptr(scale),
-             _ptr(sums), n, _ptr(codes), _ptr(grid), qbits, d_in, d_out, _ptr(Y), y_bf16, _ptr(dev_info))
+    _token_codes(n, d_in, Xq, scale, sums)
+    if not (codes.shape[1] == d_in and grid.shape == (d_out, 2) and Y.shape == (n, d_out) and codes.is_contiguous()
+            and grid.is_contiguous() and Y.is_contiguous()):
+        raise ValueError("codes must be [d_out, d_in], grid [d_out, 2] and Y [n, d_out], all contiguous")
+    _enqueue("sgpt_linear_i8", dev, stream, Xq.data_ptr(), scale.data_ptr(), sums.data_ptr(), n, codes.data_ptr(),
+             grid.data_ptr(), qbits, d_in, d_out, Y.data_ptr(), y_bf16, dev_info.data_ptr())
 
 
-def _heads(t: torch.Tensor, name: str) -> int:
-    """Row stride of [rows, heads, width] with consecutive heads."""
-    _dev(t, torch.bfloat16, name)
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _heads_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a bf16 [rows, heads, width] with consecutive heads."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must be [rows, heads, width] with consecutive heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.Tensor, O: torch.Tensor,
@@ -521,17 +534,19 @@ def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.
     may be strided, e.g. parts of one q/k/v buffer), offsets [n_seq + 1] int32
     on the device: sequence s has the rows offsets[s]:offsets[s + 1]. scale:
     width ** -0.5 when None."""
-    ldq, ldk, ldv, ldo = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V"), _heads(O, "O")
-    _dev(offsets, torch.int32, "offsets")
-    n, heads, width = Q.shape
+    dev = _one_device(Q, K, V, offsets, O, dev_info)
+    ldq, ldk, ldv, ldo = _heads_stride(Q, "Q"), _heads_stride(K, "K"), _heads_stride(V, "V"), _heads_stride(O, "O")
+    n, heads, width = shape = Q.shape
     kv_heads = K.shape[1]
-    if K.shape != (n, kv_heads, width) or V.shape != K.shape or O.shape != Q.shape:
+    if not (O.shape == shape and K.shape == (n, kv_heads, width) and V.shape == K.shape):
         raise ValueError("Q and O must be [n_tok, heads, width], K and V [n_tok, kv_heads, width]")
+    if offsets.dtype is not torch.int32:
+        raise TypeError("offsets must be int32")
     if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be contiguous [n_seq + 1]")
-    _enqueue("sgpt_attention", _one_device(Q, K, V, O, offsets, dev_info), stream, _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv,
-             _ptr(offsets), offsets.shape[0] - 1, n, heads, kv_heads, width, width ** -0.5 if scale is None else scale,
-             _ptr(O), ldo, _ptr(dev_info))
+    _enqueue("sgpt_attention", dev, stream, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, offsets.data_ptr(),
+             offsets.shape[0] - 1, n, heads, kv_heads, width, width ** -0.5 if scale is None else scale, O.data_ptr(),
+             ldo, dev_info.data_ptr())
 
 
 def mlp_block_workspace(hidden: int, inter: int, n_tok: int, device="cuda") -> torch.Tensor:
