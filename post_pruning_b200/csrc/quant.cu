@@ -48,8 +48,79 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// A sum with kRound (1.5 * 2^23) is rounded to an integer, ties to even, and
+// holds it in its low bits. (The conversion instruction shares the quarter
+// rate unit with the gate's exponential and reciprocal.)
+constexpr float kRound = 12582912.f;
+
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Eight gated values and the largest magnitude's bits so far.
+__device__ __forceinline__ void gated8(const uint4& graw, const uint4& uraw, float* z, uint32_t& top) {
+  const uint32_t g[4] = {graw.x, graw.y, graw.z, graw.w};
+  const uint32_t u[4] = {uraw.x, uraw.y, uraw.z, uraw.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    z[2 * j] = silu_mul(bf16_lo(g[j]), bf16_lo(u[j]));
+    z[2 * j + 1] = silu_mul(bf16_hi(g[j]), bf16_hi(u[j]));
+    top = max(top, max(__float_as_uint(z[2 * j]) & 0x7fffffffu, __float_as_uint(z[2 * j + 1]) & 0x7fffffffu));
+  }
+}
+
+// What a row's codes need of its largest magnitude (given by its bits).
+struct RowScale {
+  float a, k, den, inv;          // code of x = rint(x k / den), inv = 1 / den
+  bool finite, some;             // all values are numbers; one is not zero
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  RowScale r;
+  r.finite = top < 0x7f800000u;
+  r.some = r.finite && top != 0u;
+  r.a = __uint_as_float(top);
+  // 127 a and 1 / a stay numbers: rows above 2^119 are scaled by 2^-8, rows
+  // below 2^-100 by 2^64, exactly (what the first flushes is far below half a code)
+  const float pre = r.a > 0x1p119f ? 0x1p-8f : r.a < 0x1p-100f ? 0x1p64f : 1.f;
+  r.k = 127.f * pre;
+  r.den = r.a * pre;
+  r.inv = r.some ? __frcp_rn(r.den) : 0.f;
+  return r;
+}
+
+// Eight codes, and their part of the row's sum.
+__device__ __forceinline__ uint2 pack8(const int (&c)[8], int& sum) {
+  const uint2 o = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+  sum = __dp4a((int)o.x, 0x01010101, sum);
+  sum = __dp4a((int)o.y, 0x01010101, sum);
+  return o;
+}
+__device__ __forceinline__ uint2 gated_codes(const float* z, const RowScale& r, int& sum) {
+  if (!r.some) return make_uint2(0, 0);
+  const float ratio = r.k * r.inv;
+  int c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = __float_as_int(fmaf(z[j], ratio, kRound));
+  return pack8(c, sum);
+}
+__device__ __forceinline__ uint2 exact_codes(const uint4& raw, const RowScale& r, int& sum) {
+  if (!r.some) return make_uint2(0, 0);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  int c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float u = (j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2])) * r.k;
+    const float q = u * r.inv;
+    c[j] = __float_as_int(fmaf(fmaf(-q, r.den, u), r.inv, q) + kRound);
+  }
+  return pack8(c, sum);
+}
+
+// A row's scale and sum, and the report of values that are not finite.
+__device__ __forceinline__ void finish_row(const RowScale& r, int sum, float* scale, int32_t* sums, int* info) {
+  *scale = r.finite ? __fdiv_rn(r.a, 127.f) : __uint_as_float(0x7fc00000u);
+  *sums = sum;
+  if (!r.finite) set_info(info, SGPT_INFO_NONFINITE);
 }
 
 // Largest of the row's v (over the group of NT threads, and the cluster).
@@ -114,17 +185,7 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
       if (v0 + i * step < vecs) rawu[i] = __ldcs(u4 + v0 + i * step);
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const uint32_t g[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      const uint32_t u[4] = {rawu[i].x, rawu[i].y, rawu[i].z, rawu[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        z[8 * i + 2 * j] = silu_mul(bf16_lo(g[j]), bf16_lo(u[j]));
-        z[8 * i + 2 * j + 1] = silu_mul(bf16_hi(g[j]), bf16_hi(u[j]));
-        top = max(top, max(__float_as_uint(z[8 * i + 2 * j]) & 0x7fffffffu,
-                           __float_as_uint(z[8 * i + 2 * j + 1]) & 0x7fffffffu));
-      }
-    }
+    for (int i = 0; i < VPT; ++i) gated8(raw[i], rawu[i], z + 8 * i, top);
   } else {
     uint32_t m2 = 0;
 #pragma unroll
@@ -140,41 +201,16 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     ptx::cluster_sync();                           // no CTA leaves while its word is read
     return;
   }
-  const bool finite = top < 0x7f800000u;
-  const float a = __uint_as_float(top);
-  // 127 a and 1 / a stay numbers: rows above 2^119 are scaled by 2^-8, rows
-  // below 2^-100 by 2^64, exactly (what the first flushes is far below half a code)
-  const float pre = a > 0x1p119f ? 0x1p-8f : a < 0x1p-100f ? 0x1p64f : 1.f;
-  const float k = 127.f * pre, den = a * pre;
-  const bool some = finite && top != 0u;
-  const float inv = some ? __frcp_rn(den) : 0.f;
-  const float ratio = GATED ? k * inv : 0.f;
-
+  const RowScale rs = row_scale(top);
   int sum = 0;
   uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     if (v0 + i * step >= vecs) continue;
-    uint2 o = make_uint2(0, 0);
-    if (some) {
-      int c[8];
-      if constexpr (GATED) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = __float2int_rn(z[8 * i + j] * ratio);
-      } else {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u = (j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2])) * k;
-          const float q = u * inv;
-          c[j] = __float2int_rn(fmaf(fmaf(-q, den, u), inv, q));
-        }
-      }
-      o = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
-      sum = __dp4a((int)o.x, 0x01010101, sum);
-      sum = __dp4a((int)o.y, 0x01010101, sum);
-    }
-    q2[v0 + i * step] = o;
+    if constexpr (GATED)
+      q2[v0 + i * step] = gated_codes(z + 8 * i, rs, sum);
+    else
+      q2[v0 + i * step] = exact_codes(raw[i], rs, sum);
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if constexpr (NT > 32) {
@@ -188,10 +224,101 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     ptx::cluster_sync();
     sum = (int)mine[1];
   }
-  if (t == 0 && part == 0) {
-    scale[row] = finite ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fc00000u);
-    sums[row] = sum;
-    if (!finite) set_info(info, SGPT_INFO_NONFINITE);
+  if (t == 0 && part == 0) finish_row(rs, sum, scale + row, sums + row, info);
+}
+
+// The gated rows above 8192 elements, when there are many. A row takes 4 bytes
+// per element in and more arithmetic than a CTA can hide behind its own loads
+// (with a row per CTA of 512 threads, 4099 x 25600 took 161 us, 3.3 TB/s):
+// persistent CTAs of 512 keep two rows of G and U in shared memory, one
+// copied in (bulk copies) while the other is quantized.
+constexpr int kGatedThreads = 512, kGatedVec = 7;
+constexpr int kGatedMax = 28672;                                     // elements: two rows fill the shared memory
+static_assert(kGatedMax <= kGatedThreads * kGatedVec * 8, "a row in registers");
+static_assert(2 * 4 * kGatedMax + 256 <= 232448, "dynamic shared memory per CTA");
+
+__global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
+    const uint16_t* __restrict__ G, const uint16_t* __restrict__ Uu, long long n, int d, long long ldg, long long ldu,
+    int8_t* __restrict__ Xq, float* __restrict__ scale, int32_t* __restrict__ sums, int* info, long long wait_cycles) {
+  extern __shared__ __align__(128) unsigned char rows_smem[];         // [2][G row, U row]
+  __shared__ uint64_t full[2];
+  __shared__ uint32_t red[2][32];
+  __shared__ int failed;
+  ptx::let_next_start();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t row_bytes = 2u * (uint32_t)d;
+  const uint32_t s0 = ptx::smem_u32(rows_smem), bar0 = ptx::smem_u32(full);
+  if (t == 0) {
+    failed = 0;
+    ptx::mbar_init(bar0, 1);
+    ptx::mbar_init(bar0 + 8, 1);
+    ptx::mbar_init_fence();
+  }
+  ptx::after_previous();
+  if (cta_info_set(info)) return;
+  auto load = [&](long long row, int b) {
+    ptx::mbar_expect(bar0 + 8 * b, 2 * row_bytes);
+    ptx::bulk_copy(s0 + 2 * b * row_bytes, G + row * ldg, row_bytes, bar0 + 8 * b);
+    ptx::bulk_copy(s0 + (2 * b + 1) * row_bytes, Uu + row * ldu, row_bytes, bar0 + 8 * b);
+  };
+  if (t == 0)
+    for (int b = 0; b < 2; ++b) {
+      const long long row = blockIdx.x + (long long)b * gridDim.x;
+      if (row < n) load(row, b);
+    }
+  const int vecs = d / 8;
+  uint32_t use = 0;
+  for (long long row = blockIdx.x; row < n; row += gridDim.x, ++use) {
+    const int b = use & 1;
+    if (!ptx::mbar_wait(bar0 + 8 * b, (use >> 1) & 1, wait_cycles)) failed = 1;
+    __syncthreads();
+    if (failed) break;
+    const uint4* g4 = reinterpret_cast<const uint4*>(rows_smem + 2 * b * row_bytes);
+    const uint4* u4 = reinterpret_cast<const uint4*>(rows_smem + (2 * b + 1) * row_bytes);
+    float z[kGatedVec * 8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kGatedVec; ++i) {
+      uint4 graw = make_uint4(0, 0, 0, 0), uraw = graw;
+      if (t + i * kGatedThreads < vecs) {
+        graw = g4[t + i * kGatedThreads];
+        uraw = u4[t + i * kGatedThreads];
+      }
+      gated8(graw, uraw, z + 8 * i, top);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();                               // and everyone has read the row
+    top = __reduce_max_sync(0xffffffffu, lane < kGatedThreads / 32 ? red[0][lane] : 0u);
+    const long long later = row + 2LL * gridDim.x;
+    if (t == 0 && later < n) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      load(later, b);
+    }
+    const RowScale rs = row_scale(top);
+    int sum = 0;
+    uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
+#pragma unroll
+    for (int i = 0; i < kGatedVec; ++i) {
+      if (t + i * kGatedThreads >= vecs) continue;
+      q2[t + i * kGatedThreads] = gated_codes(z + 8 * i, rs, sum);
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) red[1][warp] = (uint32_t)sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = __reduce_add_sync(0xffffffffu, lane < kGatedThreads / 32 ? (int)red[1][lane] : 0);
+      if (lane == 0) finish_row(rs, sum, scale + row, sums + row, info);
+    }
+  }
+  if (failed) {
+    // the copies in flight land before the CTA ends
+    if (t == 0) {
+      for (uint32_t x = use; x < use + 2; ++x)
+        if (blockIdx.x + (long long)x * gridDim.x < n) ptx::mbar_wait(bar0 + 8 * (x & 1), (x >> 1) & 1, kDrainCycles);
+      set_info(info, SGPT_INFO_TIMEOUT);
+    }
+    __syncthreads();
   }
 }
 
@@ -228,6 +355,17 @@ cudaError_t launch_as(const uint16_t* X, const uint16_t* U, long long n, int d, 
                       NT == 32 ? 256 : NT, 0, CL, st, X, U, n, d, ldx, ldu, Xq, scale, sums, info);
 }
 
+cudaError_t launch_gated(const uint16_t* G, const uint16_t* U, long long n, int d, long long ldg, long long ldu,
+                         int8_t* Xq, float* scale, int32_t* sums, int* info, cudaStream_t st) {
+  static PerDevice attrs;
+  const cudaError_t e = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(quant_gated_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * kGatedMax);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_after(quant_gated_kernel, (unsigned)std::min<long long>(n, kNumSMs), kGatedThreads, 2 * 4 * (size_t)d, 1,
+                      st, G, U, n, d, ldg, ldu, Xq, scale, sums, info, wait_limit_cycles());
+}
+
 constexpr int kFewRows = 64;   // rows that do not fill the SMs with a CTA each
 
 template <bool GATED>
@@ -238,6 +376,8 @@ cudaError_t launch(const uint16_t* X, const uint16_t* U, long long n, int d, lon
   if (d <= 4096) return as(launch_as<128, 4, 1, GATED>);
   if (d <= 8192) return as(launch_as<256, 4, 1, GATED>);
   if (n <= kFewRows) return as(launch_as<256, 2, 8, GATED>);
+  if constexpr (GATED)
+    if (d > 16384 && d <= kGatedMax) return launch_gated(X, U, n, d, ldx, ldu, Xq, scale, sums, info, st);
   if (d <= 16384) return as(launch_as<256, 8, 1, GATED>);
   if constexpr (GATED) return as(launch_as<512, 8, 1, GATED>);
   if (d <= 26624) return as(launch_as<256, 13, 1, false>);

@@ -77,6 +77,13 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uin
       : "memory");
 }
 
+// Contiguous global -> shared (16-byte aligned, bytes % 16 == 0).
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // --------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
