@@ -371,13 +371,14 @@ sgpt_status sgpt_quant_codes(const float* W, int d_out, int d_in, int ldw, const
  * ties to even, and sums[t] = sum_k Xq[t][k]. The division is IEEE fp32; for
  * bf16 X the codes are the exact ones. A row of zeros has scale 0. A row with
  * a NaN or an infinity sets SGPT_INFO_NONFINITE (and gets codes 0, scale
- * NaN). 0 <= n <= 2^30; n == 0 launches nothing. X, Xq and the outputs must
- * not overlap. */
+ * NaN). 0 <= n <= 2^30; n == 0 launches nothing. Inputs and outputs must not
+ * overlap. */
 sgpt_status sgpt_quant_tokens(const uint16_t* X, int64_t n, int d, int64_t ldx, int8_t* Xq, float* scale,
                               int32_t* sums, int* dev_info, void* stream);
 
 /* The same for the gated input of an MLP's down projection: row t is
- * silu(G[t]) * U[t], silu(g) = g / (1 + e^-g), formed in fp32 and quantized
+ * silu(G[t]) * U[t], silu(g) = g / (1 + e^-g), formed in fp32 (a g below -87,
+ * where 1 / (1 + e^-g) leaves fp32's normal range, gives 0) and quantized
  * without rounding it to bf16 first. G and U [n x d] bf16 with leading
  * dimensions ldg, ldu (multiples of 8): two halves of one buffer are fine. */
 sgpt_status sgpt_quant_tokens_silu(const uint16_t* G, const uint16_t* U, int64_t n, int d, int64_t ldg, int64_t ldu,
@@ -416,6 +417,44 @@ sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* 
 sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
                            int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
                            int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream);
+
+/* The attention part of a decoder block pruned layer by layer, as
+ * sgpt_prune_mlp_block prunes the MLP part (same modes, parameters, rounding
+ * and errors), on packed prompts:
+ *   x -> x' = x + W_o attn(W_q x, W_k x, W_v x),
+ * q, k, v and the attention's output a rounded to bf16, attn =
+ * sgpt_attention with `scale` over the sequences of `offsets` (n_seq + 1
+ * device words).
+ *   SGPT_DRIVER_SEQUENTIAL: q, k and v are pruned from x (one Hessian and
+ *     factor), a is formed with the PRUNED q, k and v, o is pruned from a,
+ *     and x' is the pruned block's output.
+ *   SGPT_DRIVER_PARALLEL: a and x' come from the DENSE block; o is pruned from
+ *     that a, its Hessian on a second stream beside q, k and v.
+ * Rows outside every sequence have a = 0, so x' = x there; they still count
+ * in x's Hessian (pass n_tok without them if they should not).
+ * blk: the four weight matrices (fp32, row-major, in: dense, out: pruned;
+ *   W_q [heads * width x hidden], W_k, W_v [kv_heads * width x hidden],
+ *   W_o [hidden x heads * width]) and their masks ([rows x cols / 32]).
+ * X, X_next [n_tok x hidden] bf16; A [n_tok x heads * width] bf16 out (o's
+ *   input), or NULL to keep it in ws.
+ * ws: sgpt_attn_block_workspace_bytes bytes (0 = bad sizes). 1 <= n_tok <=
+ * 2^30; heads * width <= 32768. */
+typedef struct sgpt_attn_block {
+  float* W_q;
+  float* W_k;
+  float* W_v;
+  float* W_o;
+  uint32_t* mask_q;
+  uint32_t* mask_k;
+  uint32_t* mask_v;
+  uint32_t* mask_o;
+} sgpt_attn_block;
+
+size_t sgpt_attn_block_workspace_bytes(int hidden, int heads, int kv_heads, int width, int64_t n_tok);
+sgpt_status sgpt_prune_attn_block(const sgpt_attn_block* blk, int hidden, int heads, int kv_heads, int width,
+                                  float scale, const uint16_t* X, int64_t n_tok, const int32_t* offsets, int n_seq,
+                                  int mode, const sgpt_params* p, uint16_t* X_next, uint16_t* A, void* ws,
+                                  size_t ws_bytes, int* dev_info, void* stream);
 
 #ifdef __cplusplus
 }

@@ -394,4 +394,42 @@ sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, in
                                     ldo, dev_info, as_stream(stream)));
 }
 
+namespace {
+bool valid_attn_block(int hidden, int heads, int kv_heads, int width, int64_t n_tok) {
+  return valid_din(hidden) && heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && (width == 64 || width == 128) &&
+         heads <= 512 && valid_din(heads * width) && n_tok >= 1 && valid_rows(n_tok);
+}
+}  // namespace
+
+size_t sgpt_attn_block_workspace_bytes(int hidden, int heads, int kv_heads, int width, int64_t n_tok) {
+  if (!valid_attn_block(hidden, heads, kv_heads, width, n_tok)) return 0;
+  return attn_block_ws_bytes(hidden, heads, kv_heads, width, n_tok);
+}
+
+sgpt_status sgpt_prune_attn_block(const sgpt_attn_block* blk, int hidden, int heads, int kv_heads, int width,
+                                  float scale, const uint16_t* X, int64_t n_tok, const int32_t* offsets, int n_seq,
+                                  int mode, const sgpt_params* p, uint16_t* X_next, uint16_t* A, void* ws,
+                                  size_t ws_bytes, int* dev_info, void* stream) {
+  if (!blk || !X || !X_next || !offsets || !dev_info || n_seq < 0) return SGPT_ERR_INVALID_ARG;
+  const void* ptrs[] = {blk->W_q, blk->W_k, blk->W_v, blk->W_o, blk->mask_q, blk->mask_k, blk->mask_v, blk->mask_o,
+                        X, X_next};
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return SGPT_ERR_INVALID_ARG;
+  if ((A && !aligned16(A)) || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return SGPT_ERR_INVALID_ARG;
+  if (width >= 1 && width != 64 && width != 128) return SGPT_ERR_UNSUPPORTED;
+  if (!valid_attn_block(hidden, heads, kv_heads, width, n_tok)) return SGPT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SGPT_ERR_INVALID_ARG;
+  if (attention_ctas(n_tok, n_seq, heads, kv_heads) > (long long)INT32_MAX) return SGPT_ERR_UNSUPPORTED;
+  if (mode != SGPT_DRIVER_SEQUENTIAL && mode != SGPT_DRIVER_PARALLEL) return SGPT_ERR_INVALID_ARG;
+  sgpt_status s = check_params(p);
+  if (s != SGPT_OK) return s;
+  if (p->forced || p->qgrid) return SGPT_ERR_INVALID_ARG;     // each layer decides its own mask and grid
+  if (p->pattern == SGPT_PATTERN_NM && (hidden % p->m || heads * width % p->m)) return SGPT_ERR_INVALID_ARG;
+  s = check_ws(ws, ws_bytes, attn_block_ws_bytes(hidden, heads, kv_heads, width, n_tok));
+  if (s != SGPT_OK) return s;
+  if ((s = sgpt_info_clear(dev_info, stream)) != SGPT_OK) return s;
+  return from_cuda(launch_prune_attn_block(*blk, hidden, heads, kv_heads, width, scale, X, n_tok, offsets, n_seq, mode,
+                                           *p, X_next, A, ws, dev_info, as_stream(stream)));
+}
+
 }  // extern "C"

@@ -11,6 +11,10 @@
 // (gemm_tc.cu), the weights of each product the bf16 rounding of the fp32
 // weights; every rounding to bf16 is to nearest even.
 //
+// The attention part of the block: x -> x + W_o attn(W_q x, W_k x, W_v x)
+// over packed prompts, pruned the same two ways (q, k and v from x, o from the
+// attention's output), with the causal attention of attention.cu between.
+//
 // Sequential: H(x), U(x) -> prune gate and up -> z = silu(x Wg^T) * (x Wu^T)
 // with the pruned gate and up -> H(z), U(z) -> prune down -> x' = x + z Wd^T.
 // Parallel: z and x' from the dense weights first; then gate/up from x and
@@ -259,6 +263,132 @@ cudaError_t launch_prune_mlp_block(const sgpt_mlp_block& blk, int h, int f, cons
   if (ej != cudaSuccess) return ej;
   if ((e = launch_factor(w.H2, n, f, p.damp, w.U2, w.inner, info, st)) != cudaSuccess) return e;
   return prune_one(blk.W_down, h, f, w.U2, blk.mask_down, w.inner);
+}
+
+// --------------------------------------------------------- attention block
+
+namespace {
+
+struct AttnWs {
+  float* H1;        // hidden x hidden: the block input's X^T X, and its factor
+  float* U1;
+  float* H2;        // dq x dq: the attention output's, and its factor
+  float* U2;
+  uint16_t* Wb;     // bf16 weights of one product at a time
+  float* F;         // n x max(dq, hidden) fp32: a product's result
+  uint16_t* Q;      // bf16 q, k, v and attention output
+  uint16_t* K;
+  uint16_t* V;
+  uint16_t* A;
+  void* inner;      // scratch of the per-layer calls
+  void* inner2;     // a second one for the side stream (parallel mode)
+};
+
+AttnWs carve_attn(void* ws, int hidden, int dq, int dk, long long n, uint16_t* A, size_t* bytes) {
+  Carve c(ws);
+  AttnWs w;
+  w.H1 = c.take<float>((size_t)hidden * hidden);
+  w.U1 = c.take<float>((size_t)hidden * hidden);
+  w.H2 = c.take<float>((size_t)dq * dq);
+  w.U2 = c.take<float>((size_t)dq * dq);
+  w.Wb = c.take<uint16_t>((size_t)hidden * dq);
+  w.F = c.take<float>((size_t)n * std::max(dq, hidden));
+  w.Q = c.take<uint16_t>((size_t)n * dq);
+  w.K = c.take<uint16_t>((size_t)n * dk);
+  w.V = c.take<uint16_t>((size_t)n * dk);
+  w.A = A ? A : c.take<uint16_t>((size_t)n * dq);
+  const size_t inner =
+      std::max({factor_ws_bytes(hidden), factor_ws_bytes(dq), prune_ws_bytes(dq, hidden), prune_ws_bytes(dk, hidden),
+                prune_ws_bytes(hidden, dq), hessian_ws_bytes(hidden, n), hessian_ws_bytes(dq, n)});
+  w.inner = c.take<unsigned char>(inner);
+  w.inner2 = c.take<unsigned char>(std::max(hessian_ws_bytes(dq, n), (size_t)256));
+  if (bytes) *bytes = c.off + 256;
+  return w;
+}
+
+// Y (bf16) = x W^T with the weights as they are now.
+cudaError_t project(const float* W, const uint16_t* X, long long n, int d_in, int d_out, uint16_t* Y, const AttnWs& w,
+                    int* info, cudaStream_t st) {
+  cudaError_t e;
+  if ((e = launch_to_bf16(W, d_in, d_out, d_in, w.Wb, info, st)) != cudaSuccess) return e;
+  if ((e = launch_linear_bf16(X, w.Wb, n, d_in, d_out, w.F, info, st)) != cudaSuccess) return e;
+  return launch_to_bf16(w.F, d_out, n, d_out, Y, info, st);
+}
+
+}  // namespace
+
+size_t attn_block_ws_bytes(int hidden, int heads, int kv_heads, int width, long long n) {
+  size_t b = 0;
+  carve_attn(nullptr, hidden, heads * width, kv_heads * width, n, nullptr, &b);
+  return b;
+}
+
+cudaError_t launch_prune_attn_block(const sgpt_attn_block& blk, int hidden, int heads, int kv_heads, int width,
+                                    float scale, const uint16_t* X, long long n, const int32_t* offsets, int n_seq,
+                                    int mode, const sgpt_params& p, uint16_t* X_next, uint16_t* A, void* ws, int* info,
+                                    cudaStream_t st) {
+  const int dq = heads * width, dk = kv_heads * width;
+  const AttnWs w = carve_attn(ws, hidden, dq, dk, n, A, nullptr);
+  cudaError_t e;
+  auto prune_one = [&](float* W, int rows, int d, const float* U, uint32_t* mask) {
+    return launch_prune(W, rows, d, d, U, p, mask, nullptr, w.inner, info, st);
+  };
+  // the attention output of the weights as they are now; rows outside every
+  // sequence are zero, so they add nothing to its Hessian or to x'
+  auto mix = [&]() -> cudaError_t {
+    cudaError_t f;
+    if ((f = project(blk.W_q, X, n, hidden, dq, w.Q, w, info, st)) != cudaSuccess) return f;
+    if ((f = project(blk.W_k, X, n, hidden, dk, w.K, w, info, st)) != cudaSuccess) return f;
+    if ((f = project(blk.W_v, X, n, hidden, dk, w.V, w, info, st)) != cudaSuccess) return f;
+    if ((f = cudaMemsetAsync(w.A, 0, (size_t)n * dq * sizeof(uint16_t), st)) != cudaSuccess) return f;
+    if (n_seq == 0) return cudaSuccess;
+    return launch_attention(w.Q, dq, w.K, dk, w.V, dk, offsets, n_seq, n, heads, kv_heads, width, scale, w.A, dq, info,
+                            st);
+  };
+  auto output = [&]() -> cudaError_t {
+    cudaError_t f;
+    if ((f = launch_to_bf16(blk.W_o, dq, hidden, dq, w.Wb, info, st)) != cudaSuccess) return f;
+    if ((f = launch_linear_bf16(w.A, w.Wb, n, dq, hidden, w.F, info, st)) != cudaSuccess) return f;
+    residual_kernel<<<grid_for(n * hidden / 4), 256, 0, st>>>(X, w.F, n * hidden, X_next, info);
+    count_launches(1);
+    return cudaGetLastError();
+  };
+  auto prune_qkv = [&]() -> cudaError_t {
+    cudaError_t f;
+    if ((f = launch_hessian_tc(w.H1, X, n, hidden, w.inner, info, st, true)) != cudaSuccess) return f;
+    if ((f = launch_factor(w.H1, n, hidden, p.damp, w.U1, w.inner, info, st)) != cudaSuccess) return f;
+    if ((f = prune_one(blk.W_q, dq, hidden, w.U1, blk.mask_q)) != cudaSuccess) return f;
+    if ((f = prune_one(blk.W_k, dk, hidden, w.U1, blk.mask_k)) != cudaSuccess) return f;
+    return prune_one(blk.W_v, dk, hidden, w.U1, blk.mask_v);
+  };
+  auto prune_o = [&]() -> cudaError_t {
+    const cudaError_t f = launch_factor(w.H2, n, dq, p.damp, w.U2, w.inner, info, st);
+    return f != cudaSuccess ? f : prune_one(blk.W_o, hidden, dq, w.U2, blk.mask_o);
+  };
+  if (mode == SGPT_DRIVER_SEQUENTIAL) {
+    if ((e = prune_qkv()) != cudaSuccess) return e;
+    if ((e = mix()) != cudaSuccess) return e;
+    if ((e = launch_hessian_tc(w.H2, w.A, n, dq, w.inner, info, st, true)) != cudaSuccess) return e;
+    if ((e = prune_o()) != cudaSuccess) return e;
+    return output();
+  }
+  // parallel: the dense block's attention output and result first
+  if ((e = mix()) != cudaSuccess) return e;
+  if ((e = output()) != cudaSuccess) return e;
+  DriverStreams* ds = nullptr;
+  std::lock_guard<std::mutex> lock(g_drv_mu);
+  if ((e = driver_streams(&ds)) != cudaSuccess) return e;
+  // the attention output's Hessian on the side stream, beside q, k and v
+  if ((e = cudaEventRecord(ds->fork, st)) != cudaSuccess) return e;
+  if ((e = cudaStreamWaitEvent(ds->side, ds->fork, 0)) != cudaSuccess) return e;
+  cudaError_t es = launch_hessian_tc(w.H2, w.A, n, dq, w.inner2, info, ds->side, true);
+  if (es == cudaSuccess) es = cudaEventRecord(ds->join, ds->side);
+  e = prune_qkv();
+  // always join the side stream, also after an error (a capture stays well formed)
+  const cudaError_t ej = es == cudaSuccess ? cudaStreamWaitEvent(st, ds->join, 0) : es;
+  if (e != cudaSuccess) return e;
+  if (ej != cudaSuccess) return ej;
+  return prune_o();
 }
 
 }  // namespace sgpt

@@ -47,6 +47,12 @@ cudaError_t launch_prune_mlp_block(const sgpt_mlp_block& blk, int h, int f, cons
                                    int mode, const sgpt_params& p, uint16_t* X_next, uint16_t* Z, void* ws,
                                    int* info, cudaStream_t st);
 
+size_t attn_block_ws_bytes(int hidden, int heads, int kv_heads, int width, long long n);
+cudaError_t launch_prune_attn_block(const sgpt_attn_block& blk, int hidden, int heads, int kv_heads, int width,
+                                    float scale, const uint16_t* X, long long n, const int32_t* offsets, int n_seq,
+                                    int mode, const sgpt_params& p, uint16_t* X_next, uint16_t* A, void* ws, int* info,
+                                    cudaStream_t st);
+
 // consumer.cu
 size_t sparse24_meta_tiles_bytes(int rows, int d);
 cudaError_t launch_tile_meta(const uint32_t* meta, int rows, int d, uint32_t* tiles, cudaStream_t st);

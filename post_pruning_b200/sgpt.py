@@ -36,6 +36,7 @@ EXPORTS = (
     "sgpt_mlp_block_workspace_bytes", "sgpt_prune_mlp_block", "sgpt_linear_bf16", "sgpt_to_bf16",
     "sgpt_sparse24_linear", "sgpt_sparse24_meta_tiles_bytes", "sgpt_sparse24_tile_meta",
     "sgpt_quant_codes", "sgpt_quant_tokens", "sgpt_quant_tokens_silu", "sgpt_linear_i8", "sgpt_attention",
+    "sgpt_attn_block_workspace_bytes", "sgpt_prune_attn_block",
 )
 DRIVER_SEQUENTIAL = 0
 DRIVER_PARALLEL = 1
@@ -97,6 +98,11 @@ class _MlpBlock(ctypes.Structure):
                 ("W_gate", "W_up", "W_down", "mask_gate", "mask_up", "mask_down")]
 
 
+class _AttnBlock(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("W_q", "W_k", "W_v", "W_o", "mask_q", "mask_k", "mask_v", "mask_o")]
+
+
 _lib = None
 
 
@@ -143,6 +149,9 @@ def lib() -> ctypes.CDLL:
         "sgpt_linear_i8": (i32, [vp, vp, vp, i64, vp, vp, i32, i32, i32, vp, i32, vp, vp]),
         "sgpt_attention": (i32, [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, ctypes.c_float, vp, i64,
                                  vp, vp]),
+        "sgpt_attn_block_workspace_bytes": (sz, [i32, i32, i32, i32, i64]),
+        "sgpt_prune_attn_block": (i32, [ctypes.POINTER(_AttnBlock), i32, i32, i32, i32, ctypes.c_float, vp, i64, vp,
+                                        i32, i32, pp, vp, vp, vp, sz, vp, vp]),
         "sgpt_recon_error": (i32, [vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]),
         "sgpt_prune_layer": (i32, [vp, i32, i32, i32, vp, i64, vp, vp, pp, vp, vp, vp, vp,
                                    vp, sz, vp, vp]),
@@ -587,6 +596,55 @@ def prune_mlp_block(W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tens
     _check(lib().sgpt_prune_mlp_block(ctypes.byref(blk), hidden, inter, _ptr(X), n, mode, ctypes.byref(p),
                                       _ptr(X_next), _ptr(Z), _ptr(ws), ws.numel(), _ptr(dev_info),
                                       _stream(stream)), "sgpt_prune_mlp_block")
+
+
+def attn_block_workspace(hidden: int, heads: int, kv_heads: int, width: int, n_tok: int,
+                         device="cuda") -> torch.Tensor:
+    b = int(lib().sgpt_attn_block_workspace_bytes(hidden, heads, kv_heads, width, n_tok))
+    if b == 0:
+        raise ValueError("unsupported block sizes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def prune_attn_block(W_q: torch.Tensor, W_k: torch.Tensor, W_v: torch.Tensor, W_o: torch.Tensor, masks,
+                     X: torch.Tensor, offsets: torch.Tensor, width: int, params: Params, X_next: torch.Tensor,
+                     ws: torch.Tensor, dev_info: torch.Tensor, mode: int = DRIVER_SEQUENTIAL,
+                     A: torch.Tensor | None = None, scale: float | None = None, stream=None):
+    """The attention part of a decoder block pruned layer by layer over packed
+    prompts (sgpt_prune_attn_block). W_q [heads * width, hidden], W_k, W_v
+    [kv_heads * width, hidden], W_o [hidden, heads * width] fp32; masks:
+    (q, k, v, o) int32 mask-bit tensors; offsets [n_seq + 1] int32; A [n_tok,
+    heads * width] bf16 receives o's input. scale: width ** -0.5 when None."""
+    dq, hidden = W_q.shape
+    dk = W_k.shape[0]
+    n = X.shape[0]
+    if width < 1 or dq % width or dk % width:
+        raise ValueError("the rows of W_q, W_k and W_v are whole heads of `width`")
+    dev = _one_device(W_q, W_k, W_v, W_o, *masks, X, offsets, X_next, ws, dev_info, *(() if A is None else (A,)))
+    for t, name, shape in ((W_q, "W_q", (dq, hidden)), (W_k, "W_k", (dk, hidden)), (W_v, "W_v", (dk, hidden)),
+                           (W_o, "W_o", (hidden, dq))):
+        _dev(t, torch.float32, name)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {shape}")
+    for t, shape in zip(masks, ((dq, hidden // 32), (dk, hidden // 32), (dk, hidden // 32), (hidden, dq // 32)),
+                        strict=True):
+        _dev(t, torch.int32, "mask")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"mask must be contiguous {shape}")
+    for t, name, shape in ((X, "X", (n, hidden)), (X_next, "X_next", (n, hidden)), (A, "A", (n, dq))):
+        if t is None:
+            continue
+        _dev(t, torch.bfloat16, name)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {shape}")
+    _dev(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous [n_seq + 1]")
+    blk = _AttnBlock(*(_ptr(t) for t in (W_q, W_k, W_v, W_o, *masks)))
+    p = params.to_c()
+    _enqueue("sgpt_prune_attn_block", dev, stream, ctypes.byref(blk), hidden, dq // width, dk // width, width,
+             width ** -0.5 if scale is None else scale, _ptr(X), n, _ptr(offsets), offsets.shape[0] - 1, mode,
+             ctypes.byref(p), _ptr(X_next), _ptr(A), _ptr(ws), ws.numel(), _ptr(dev_info))
 
 
 def pack_nm_meta_words(d_in: int, n: int, m: int) -> int:
