@@ -168,15 +168,22 @@ struct Work {
   __device__ int blocks(const Shape& sh, int h) const { return row(sh, h) < len ? row(sh, h) / kT + 1 : 0; }
 };
 
-// The unit `index` of the launch, by a whole warp. A sequence's offsets are
-// used only if they lie inside the packed rows.
-__device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lane) {
+// Where the last search ended: the first of 32 sequences, and the units before it.
+struct Search {
+  int b0 = 0, before = 0;
+};
+
+// The unit `index` of the launch, by a whole warp, which goes on from its last
+// search (a CTA's indices mostly grow). A sequence's offsets are used only if
+// they lie inside the packed rows.
+__device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lane, Search& at_seq) {
   const int head_units = sh.pair ? sh.heads / 2 : sh.heads;
   const int unit_rows = sh.pair ? kT : 2 * kT;
   const int unit = index / head_units;
   Work w{0, 0, 0, index % head_units};
-  int before = 0;
-  for (int b0 = 0; b0 < sh.n_seq; b0 += 32) {
+  if (unit < at_seq.before) at_seq = Search();
+  int before = at_seq.before;
+  for (int b0 = at_seq.b0; b0 < sh.n_seq; b0 += 32) {
     const int b = b0 + lane;
     int first = 0, len = 0;
     if (b < sh.n_seq) {
@@ -198,6 +205,8 @@ __device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lan
       w.first = __shfl_sync(0xffffffffu, first, src);
       w.len = __shfl_sync(0xffffffffu, len, src);
       w.unit = __shfl_sync(0xffffffffu, units - 1 - at, src);      // the longest rows of keys first
+      at_seq.b0 = b0;
+      at_seq.before = before;
       return w;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
@@ -271,7 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   }
   let_next_start();
   after_previous();
-  if (cta_info_set(info)) return;
   if (blockIdx.x == 0) {                         // every offset is checked once
     bool bad = false;
     for (int b = threadIdx.x; b < sh.n_seq; b += kThreads) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
@@ -293,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       uint32_t q_used[2] = {0, 0};
       bool ok = true, asked = false;
       Phase answers;
+      Search at_seq;
       while (ok) {
-        const Work w = index < 0 ? Work{0, 0, 0, 0} : find_work(sh, cu, index, lane);
+        const Work w = index < 0 ? Work{0, 0, 0, 0} : find_work(sh, cu, index, lane, at_seq);
         if (index >= 0) {
           if (lane == 0) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the last answer has been read
@@ -472,6 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const uint64_t c2 = pair_of(sh.c, sh.c);
     Phase sn, on;
     bool ok = true;
+    // an error recorded by an earlier call: everything runs, nothing is
+    // written (the look at *info is under the first products)
+    const bool write = !info_set(info);
     auto wait = [&](uint32_t bar, uint32_t parity) {       // one decision for the warp
       ok = !__any_sync(0xffffffffu, !mbar_wait(bar, parity, wait_cycles));
       fence_after();
@@ -563,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           bad = fma2(y, 0, bad);
           v[e] = pack_bf16(pair_to(y).x, pair_to(y).y);
         }
-        if (row < w.len) {
+        if (row < w.len && write) {
           store32(op + 32 * i, v, sh.wide);
           store32(op + 32 * i + 16, v + 8, sh.wide);
         }

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
   float* tok_scale = reinterpret_cast<float*>(smem + kStages * kStage + 256);       // [2][BN]
   int32_t* tok_sum = reinterpret_cast<int32_t*>(tok_scale + 2 * BN);                // [2][BN]
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed, skip;
+  __shared__ int failed;
   let_next_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank(), leader = rank & ~1u, half = rank & 1u;   // the pair's first CTA; this one's half
@@ -232,23 +232,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
-  if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
   if (warp == 1 && lane == 0) {
     int mt, nt;
     decode(first_item, mt, nt);
     for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * 2 * kBM + (int)half * kBM);
   }
   after_previous();
-  if (threadIdx.x == 0) skip = info_set(info);
+  if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
   fence_before();
   cluster_sync();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  // one decision for the cluster: its first CTA's look at *info
-  const bool run = ld_cluster(map_rank(smem_u32(&skip), 0)) == 0;
+  // an error recorded by an earlier call: everything runs, nothing is written
+  // (the look at *info is under the products)
+  const bool write = warp < 2 || !info_set(info);
 
   if (warp == 0) {
-    if (run && elect_one()) {
+    if (elect_one()) {
       const uint32_t leader_full0 = map_rank(full0, leader);
       long long g = 0;
       for (long long w = first_item; w < items && !failed; w += step) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
       }
     }
   } else if (warp == 1) {
-    if (half == 0 && run && elect_one()) {
+    if (half == 0 && elect_one()) {
       const uint64_t a_desc = sw128_desc(s0), b_desc = sw128_desc(s0 + kABytes);
       long long g = 0;
       int u = 0;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
       mma_commit2(mdone, both);
       if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
     }
-  } else if (run) {
+  } else {
     const int q = warp & 3, et = threadIdx.x - 64;       // TMEM lanes 32 q .. of this warp; epilogue thread
     const uint32_t leader_tempty0 = map_rank(tempty0, leader);
     int u = 0;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
           if (split > 1) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) part[(c + e) * kBM] = (int32_t)v[e];
-          } else if (row < rows) {
+          } else if (row < rows && write) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               if (c + e < cols) store_y(yp, result((int)v[e], ch, tok_scale[b * BN + c + e], tok_sum[b * BN + c + e]));
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
   }
   if (split > 1) {                              // one tile per cluster
     cluster_sync();
-    bool all = run;
+    bool all = write;
     for (int p = 0; p < 2 * split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
     if (warp >= 2 && all) {
       int mt, nt;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed, skip;
+  __shared__ int failed;
   __shared__ float tok_scale[BN];
   __shared__ int32_t tok_sum[BN];
   let_next_start();
@@ -422,19 +422,18 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
-  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
   if (warp == 1 && lane == 0)
     for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * kBM);
   after_previous();
-  if (threadIdx.x == 0) skip = info_set(info);
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  const bool run = skip == 0;
+  const bool write = warp < 2 || !info_set(info);            // as above
 
   if (warp == 0) {
-    if (lane == 0 && run) {
+    if (elect_one()) {
       int g = 0;
       for (int i = k0; i < k1; ++i, ++g) {
         const int s = g % kStages;
@@ -452,7 +451,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
         if (!mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, kDrainCycles)) failed = 1;
     }
   } else if (warp == 1) {
-    if (lane == 0 && run) {
+    if (elect_one()) {
+      const uint64_t a_desc = sw128_desc(s0), b_desc = sw128_desc(s0 + kABytes);
       for (int g = 0; g < k1 - k0; ++g) {
         const int s = g % kStages;
         if (!mbar_wait(full0 + 8 * s, (g / kStages) & 1, wait_cycles)) {
@@ -460,11 +460,10 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
           break;
         }
         fence_after();
-        const uint32_t sa = s0 + s * kStage;
+        const uint64_t off = (uint64_t)(s * kStage >> 4);
 #pragma unroll
         for (int j = 0; j < kBK / 32; ++j)
-          mma_i8<0>(tmem, sw128_desc(sa + 32 * j), sw128_desc(sa + kABytes + 32 * j), idesc(kBM, BN),
-                    (g > 0 || j > 0) ? 1u : 0u);
+          mma_i8<0>(tmem, a_desc + off + 2 * j, b_desc + off + 2 * j, idesc(kBM, BN), j > 0 ? 1u : (uint32_t)(g > 0));
         mma_commit(empty0 + 8 * s);
       }
       if (!failed) mma_commit(tfull);
@@ -478,8 +477,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
   T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
   Channel ch{0.f, 0};
-  bool ok = run;
-  if (warp >= 2 && run) {
+  bool ok = true;
+  if (warp >= 2) {
     for (int e = threadIdx.x - 64; e < cols; e += 128) {
       tok_scale[e] = out.xs[n0 + e];
       tok_sum[e] = out.xsum[n0 + e];
@@ -499,7 +498,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
         uint32_t v[16];
         tmem_ld16(lanes + c, v);
         tmem_ld_wait();
-        if (row >= rows) continue;
+        if (row >= rows || !write) continue;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (c + e < cols) store_y(Y + (long long)(c + e) * rows, result((int)v[e], ch, tok_scale[c + e], tok_sum[c + e]));
@@ -521,9 +520,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
       }
     }
     cluster_sync();
-    bool all = true;
-    for (int p = 0; p < split; ++p)
-      all = all && (ld_cluster(map_rank(smem_u32(&failed), p)) | ld_cluster(map_rank(smem_u32(&skip), p))) == 0;
+    bool all = write;
+    for (int p = 0; p < split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
     if (warp >= 2 && all) add_parts<T>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, tok_scale, tok_sum);
     cluster_sync();                                        // no CTA leaves while its sums are read
   }

@@ -160,12 +160,9 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
   const int part = CL > 1 ? (int)ptx::cluster_rank() : 0;
   ptx::let_next_start();
   ptx::after_previous();
-  const bool skip = cta_info_set(info);
-  if (CL == 1 && skip) return;
   const int t = threadIdx.x % NT;
   const long long row = (long long)(blockIdx.x / CL) * kRows + threadIdx.x / NT;
-  if (kRows > 1 && row >= n) return;
-  const int vecs = d / 8, v0 = part * NT + t, step = NT * CL;
+  const int vecs = kRows > 1 && row >= n ? 0 : d / 8, v0 = part * NT + t, step = NT * CL;
   const uint4* x4 = reinterpret_cast<const uint4*>(X + row * ldx);
   const uint4* u4 = reinterpret_cast<const uint4*>(GATED ? Uu + row * ldu : nullptr);
 
@@ -177,13 +174,17 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     raw[i] = make_uint4(0, 0, 0, 0);
     if (v0 + i * step < vecs) raw[i] = __ldcs(x4 + v0 + i * step);
   }
+  uint4 rawu[GATED ? VPT : 1];
   if constexpr (GATED) {
-    uint4 rawu[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       rawu[i] = make_uint4(0, 0, 0, 0);
       if (v0 + i * step < vecs) rawu[i] = __ldcs(u4 + v0 + i * step);
     }
+  }
+  const bool skip = cta_info_set(info);            // under the row's loads
+  if (CL == 1 && (skip || vecs == 0)) return;
+  if constexpr (GATED) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) gated8(raw[i], rawu[i], z + 8 * i, top);
   } else {
@@ -255,7 +256,6 @@ __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
     ptx::mbar_init_fence();
   }
   ptx::after_previous();
-  if (cta_info_set(info)) return;
   auto load = [&](long long row, int b) {
     ptx::mbar_expect(bar0 + 8 * b, 2 * row_bytes);
     ptx::bulk_copy(s0 + 2 * b * row_bytes, G + row * ldg, row_bytes, bar0 + 8 * b);
@@ -268,6 +268,12 @@ __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
     }
   const int vecs = d / 8;
   uint32_t use = 0;
+  if (cta_info_set(info)) {                        // under the first copies, which land before the CTA ends
+    if (t == 0)
+      for (int b = 0; b < 2; ++b)
+        if (blockIdx.x + (long long)b * gridDim.x < n) ptx::mbar_wait(bar0 + 8 * b, 0, kDrainCycles);
+    return;
+  }
   for (long long row = blockIdx.x; row < n; row += gridDim.x, ++use) {
     const int b = use & 1;
     if (!ptx::mbar_wait(bar0 + 8 * b, (use >> 1) & 1, wait_cycles)) failed = 1;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -170,6 +171,8 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // prefetches into the L2, which is coherent, excepted: a prefetch only). Its
 // predecessor lets it start by let_next_start() (or by ending); the
 // predecessor's results are complete and visible after after_previous() only.
+// TMEM is allocated after it too: a CTA that held some while it waited could
+// keep a predecessor's CTA on the same SM from ever getting its own.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -278,17 +281,20 @@ typedef CUresult (*TmaEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// cuTensorMapEncodeTiled of the installed driver, looked up once.
+// cuTensorMapEncodeTiled of the installed driver, looked up until it is found.
 inline TmaEncodeFn tma_encode_fn() {
-  static const TmaEncodeFn fn = []() -> TmaEncodeFn {
+  static std::atomic<TmaEncodeFn> fn{nullptr};
+  TmaEncodeFn f = fn.load(std::memory_order_acquire);
+  if (!f) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<TmaEncodeFn>(p);
-    return nullptr;
-  }();
-  return fn;
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<TmaEncodeFn>(p);
+      fn.store(f, std::memory_order_release);
+    }
+  }
+  return f;
 }
 
 // Launches f with clusters of `cluster` CTAs, allowed to start before its

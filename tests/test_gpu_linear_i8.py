@@ -313,6 +313,27 @@ def test_linear_i8_wait_times_out():
     _check_linear(Y, whole, s, grid)
 
 
+def test_gated_rows_wait_times_out():
+    """The copies of long gated rows, as above."""
+    G = torch.randn(200, 25600, device=DEV, generator=_gen(6)).bfloat16()
+    q, s, t = _tokens(200, 25600)
+    info = pp.new_info()
+    pp.quant_tokens_silu(G, G, q, s, t, info)
+    pp.raise_on_info(info)
+    want = q.clone()
+    pp.set_wait_limit(1)
+    try:
+        pp.quant_tokens_silu(G, G, q, s, t, info)
+        assert pp.sync_status(info) == 4                  # TIMEOUT
+    finally:
+        pp.set_wait_limit(0)
+    pp.info_clear(info)
+    q.zero_()
+    pp.quant_tokens_silu(G, G, q, s, t, info)
+    pp.raise_on_info(info)
+    assert torch.equal(q, want)
+
+
 def test_pruned_and_quantized_layer_runs_as_integers():
     """The sweep's joint result through the integer forward: its codes stand
     for the pruned weights exactly, so Y is X's 8-bit form times them."""
