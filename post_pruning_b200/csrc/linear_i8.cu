@@ -97,7 +97,6 @@ __device__ __forceinline__ Channel channel(const Out& o, int row) {
 }
 
 constexpr int kMaxSplit = 8;                    // parts of K at most
-constexpr int kAhead = 8;                       // stages of codes fetched into the L2 before the predecessor has ended
 
 // y of one token and channel from the exact sum of products.
 __device__ __forceinline__ float result(int sum, const Channel& ch, float tok_scale, int tok_sum) {
@@ -124,12 +123,9 @@ __device__ __forceinline__ void store4(uint16_t* y, const float (&v)[4]) {
 // time, 16 loads in flight, are what keeps this short.
 template <class T>
 __device__ __forceinline__ void add_parts(uint32_t part, int split, int sp, int first, int step, int w, int lane,
-                                          int row0, int n0, int cols, const Out& out, const float* tok_scale,
-                                          const int32_t* tok_sum) {
+                                          int row0, int n0, int cols, const Out& out, const Channel (&ch)[4],
+                                          const float* tok_scale, const int32_t* tok_sum) {
   const int rows = out.rows, row = row0 + 4 * lane;
-  Channel ch[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x) ch[x] = channel(out, row + x);
   const bool whole = rows % 4 == 0 && row + 3 < rows;
   T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
   const int every = 4 * split;
@@ -231,11 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
     }
     mbar_init(mdone, 1);
     mbar_init_fence();
-  }
-  if (warp == 1 && lane == 0) {
-    int mt, nt;
-    decode(first_item, mt, nt);
-    for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * 2 * kBM + (int)half * kBM);
   }
   after_previous();
   if (warp == 0) tmem_alloc2(smem_u32(&tmem_slot), 2 * BN);
@@ -348,15 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
     }
   }
   if (split > 1) {                              // one tile per cluster
+    int mt, nt;
+    decode(first_item, mt, nt);
+    const int row0 = mt * 2 * kBM + (int)half * kBM;
+    Channel ch4[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, row0 + 4 * lane + x);
     cluster_sync();
     bool all = write;
     for (int p = 0; p < 2 * split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
-    if (warp >= 2 && all) {
-      int mt, nt;
-      decode(first_item, mt, nt);
-      add_parts<T>(s0, split, sp, (int)half, 2, warp - 2, lane, mt * 2 * kBM + (int)half * kBM, nt * BN,
-                   min(BN, n - nt * BN), out, tok_scale, tok_sum);
-    }
+    if (warp >= 2 && all)
+      add_parts<T>(s0, split, sp, (int)half, 2, warp - 2, lane, row0, nt * BN, min(BN, n - nt * BN), out, ch4, tok_scale,
+                   tok_sum);
   }
   __syncwarp();
   fence_before();
@@ -376,21 +370,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
 // ---------------------------------------------------- one tile, split over K
 
 
-constexpr int kSplitStages = 4;
+// the most that leaves room for two CTAs on an SM
+__host__ __device__ constexpr int split_stages(int bn) { return bn <= 16 ? 6 : bn <= 32 ? 5 : 4; }
 __host__ __device__ constexpr int split_stage(int bn) { return kABytes + bn * kBK; }
 __host__ __device__ constexpr size_t split_smem(int bn) {
-  return (size_t)kSplitStages * split_stage(bn) + 1024 + 128;
+  return (size_t)split_stages(bn) * split_stage(bn) + 1024 + 128;
 }
-// CTAs that fit on an SM together
-__host__ __device__ constexpr int split_per_sm(int bn) { return bn <= 16 ? 3 : 2; }
-static_assert(3 * (split_smem(16) + 1280) <= 233472 && 2 * (split_smem(64) + 1664) <= 233472, "CTAs per SM");
+constexpr int kSplitPerSM = 2;
+static_assert(2 * (split_smem(16) + 2048) <= 233472 && 2 * (split_smem(32) + 2048) <= 233472 &&
+                  2 * (split_smem(64) + 2048) <= 233472, "CTAs per SM");
 
 template <int BN, class T>
 __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                    const __grid_constant__ CUtensorMap xmap, int d,
                                                                    int split, const Out out, int* info,
                                                                    const long long wait_cycles) {
-  constexpr int kStages = kSplitStages, kStage = split_stage(BN);
+  constexpr int kStages = split_stages(BN), kStage = split_stage(BN);
   constexpr uint32_t kCols = BN < 32 ? 32 : BN;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -422,8 +417,6 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     mbar_init(mdone, 1);
     mbar_init_fence();
   }
-  if (warp == 1 && lane == 0)
-    for (int i = k0; i < min(k1, k0 + kAhead); ++i) prefetch_2d(&wmap, i * kBK, mt * kBM);
   after_previous();
   if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kCols);
   fence_before();
@@ -476,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   const int row = mt * kBM + r, n0 = nt * BN, cols = min(BN, n - n0);
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
   T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
-  Channel ch{0.f, 0};
+  Channel ch{0.f, 0}, ch4[4];                              // this lane's channel, or its four of the split sums
   bool ok = true;
   if (warp >= 2) {
     for (int e = threadIdx.x - 64; e < cols; e += 128) {
@@ -484,6 +477,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
       tok_sum[e] = out.xsum[n0 + e];
     }
     ch = channel(out, row);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, mt * kBM + 4 * lane + x);
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (__any_sync(0xffffffffu, !mbar_wait(tfull, 0, wait_cycles))) {
       failed = 1;
@@ -522,7 +517,7 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     cluster_sync();
     bool all = write;
     for (int p = 0; p < split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
-    if (warp >= 2 && all) add_parts<T>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, tok_scale, tok_sum);
+    if (warp >= 2 && all) add_parts<T>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, ch4, tok_scale, tok_sum);
     cluster_sync();                                        // no CTA leaves while its sums are read
   }
   fence_before();
@@ -595,8 +590,11 @@ cudaError_t launch_split(const Args& a) {
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, BN);
   const int kt = cdiv(a.d, kBK);
+  // parts of K: as many as find room on the GPU together (a power of two:
+  // clusters of seven took a third longer than clusters of four), of two
+  // stages at least
   int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * split_per_sm(BN) && split * 2 <= kt) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * kSplitPerSM && split * 2 <= kt) split *= 2;
   if (tiles * split > INT32_MAX) return cudaErrorInvalidValue;
   return launch_after(linear_i8_split_kernel<BN, T>, (unsigned)(tiles * split), kThreads, split_smem(BN), split, a.st, wm,
                       xm, a.d, split, a.out, a.info, wait_limit_cycles());

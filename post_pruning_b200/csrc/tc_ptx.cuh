@@ -167,21 +167,12 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 //
 // A kernel launched with launch_after() may start while its predecessor in the
 // stream still runs, and must call after_previous() in every CTA before it
-// touches anything in global memory that others write (reads of *info and
-// prefetches into the L2, which is coherent, excepted: a prefetch only). Its
-// predecessor lets it start by let_next_start() (or by ending); the
+// touches global memory. Its predecessor lets it start by let_next_start() (or by ending); the
 // predecessor's results are complete and visible after after_previous() only.
 // TMEM is allocated after it too: a CTA that held some while it waited could
 // keep a predecessor's CTA on the same SM from ever getting its own.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// The box's bytes into the L2.
-__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y)
-               : "memory");
-}
 
 // ---------------------------------------------------------- grid as a queue
 //
