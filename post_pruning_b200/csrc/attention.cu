@@ -225,6 +225,33 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* v, bool wid
   }
 }
 
+// Transposes four 32-byte pieces of a row over the four lanes of a quad: in,
+// lane x has the pieces 0..3 of row x; out, lane x has piece x of the rows
+// 0..3. A store then writes 128 consecutive bytes of eight rows instead of 32
+// bytes of each of 32 rows, a quarter of the lines. For a width of 128 those
+// lines took 1900 of the epilogue's 2700 cycles (8 x 2048 rows, 64 heads on 8:
+// 526 -> 517 us at full clocks). It costs more than it saves for a width of 64 (half the
+// lines) and in units of one or two blocks, whose epilogue nothing hides.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[32], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool odd = lane & bit;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & bit) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int lo = 8 * a + i, hi = 8 * (a | bit) + i;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[lo] : v[hi], bit);
+        if (odd)
+          v[lo] = got;
+        else
+          v[hi] = got;
+      }
+    }
+  }
+}
+
 // One wait's count on a barrier: the n-th wait takes parity n & 1.
 struct Phase {
   uint32_t n = 0;
@@ -563,21 +590,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       uint64_t bad = 0;                                    // a sum of o * 0: NaN if one is not finite
       const uint64_t inv2 = pair_of(inv, inv);
       uint16_t* op = O + (long long)(w.first + row) * sh.ldo + w.head(sh, h) * D;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
+      auto chunk = [&](int i, uint32_t* v) {               // 32 columns of the row
         uint32_t o[32];
         tmem_ld32(to + 32 * i, o);
         tmem_ld_wait();
-        uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint64_t y = fma2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2, 0);
           bad = fma2(y, 0, bad);
           v[e] = pack_bf16(pair_to(y).x, pair_to(y).y);
         }
-        if (row < w.len && write) {
-          store32(op + 32 * i, v, sh.wide);
-          store32(op + 32 * i + 16, v + 8, sh.wide);
+      };
+      if (D == 128 && mine > 2) {
+        const int quad = lane & 3;
+        // a warp without a row of the sequence has nothing to write
+#pragma unroll 1
+        for (int i = row - lane < w.len ? 0 : 2; i < 2; ++i) {
+          uint32_t v[32];
+          chunk(2 * i, v);
+          chunk(2 * i + 1, v + 16);
+          quad_transpose(v, lane);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (row - quad + x < w.len && write) store32(op + (x - quad) * sh.ldo + 64 * i + 16 * quad, v + 8 * x, sh.wide);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t v[16];
+          chunk(i, v);
+          if (row < w.len && write) {
+            store32(op + 32 * i, v, sh.wide);
+            store32(op + 32 * i + 16, v + 8, sh.wide);
+          }
         }
       }
       fence_before();                                      // O is read: the next unit's weights follow
