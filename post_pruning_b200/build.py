@@ -1,10 +1,12 @@
-"""Build libsgpt.so (the C-ABI solver library) in-tree with nvcc for sm_100a.
+"""Build libsgpt.so (the C-ABI solver library) in-tree with nvcc for sm_100a,
+and the binding's argument marshalling (_marshal, host code) with the C++
+compiler.
 
     python -m post_pruning_b200.build [--verbose-ptxas]
 
 Objects go to post_pruning_b200/_build/, the library to
-post_pruning_b200/libsgpt.so. Only sources newer than their object are
-recompiled.
+post_pruning_b200/libsgpt.so, the extension module beside it. Only sources
+newer than their object are recompiled.
 """
 
 from __future__ import annotations
@@ -15,11 +17,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsgpt.so")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,11 +60,32 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
     return obj
 
 
+def _build_marshal() -> None:
+    """csrc/marshal.cpp against the installed torch's headers (host code only)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgpt.h")))
+    if os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-I" + d for d in (os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+                                sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
+           src, "-o", MARSHAL, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(ptxas_verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
+        marshal.result()
     if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
         return LIB
     cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"]

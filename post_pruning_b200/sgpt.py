@@ -104,6 +104,7 @@ class _AttnBlock(ctypes.Structure):
 
 
 _lib = None
+_marshal = None         # the extension module that marshals the hot calls' arguments
 
 
 def lib() -> ctypes.CDLL:
@@ -160,7 +161,11 @@ def lib() -> ctypes.CDLL:
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
-    _lib = L
+    global _marshal
+    from . import _marshal as m        # built with the library; missing: ImportError
+    m.bind(*(ctypes.cast(getattr(L, "sgpt_" + name), vp).value for name in
+             ("quant_tokens", "quant_tokens_silu", "linear_i8", "attention")))
+    _lib, _marshal = L, m
     return L
 
 
@@ -463,8 +468,12 @@ def quant_codes(W: torch.Tensor, grid: torch.Tensor, codes: torch.Tensor, dev_in
              _ptr(codes), _ptr(dev_info))
 
 
-# The checks of the calls below are written for a call that takes a few
-# microseconds in all: one expression for the types, one for the shapes.
+# The calls below are made once per token and layer, and checking their
+# arguments here takes longer than launching them. So the extension module
+# (csrc/marshal.cpp) is asked first: it makes the same checks and the call,
+# and answers the status, or -1 where the arguments are not plainly valid (or
+# on another device than the current one); then they are checked again here,
+# to raise what is wrong with them or to make the call.
 
 def _token_codes(n: int, d: int, Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor):
     """Xq [n, d] int8, scale [n] fp32, sums [n] int32, contiguous."""
@@ -479,6 +488,12 @@ def quant_tokens(X: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: t
                  dev_info: torch.Tensor, stream=None):
     """X [n, d] bf16 to 8 bits with a scale per token (sgpt_quant_tokens):
     Xq [n, d] int8, scale [n] fp32, sums [n] int32 (the codes' row sums)."""
+    if stream is None and _marshal is not None:
+        status = _marshal.quant_tokens(X, Xq, scale, sums, dev_info)
+        if status == SGPT_OK:
+            return
+        if status > 0:
+            raise SgptError(status, "sgpt_quant_tokens")
     dev = _one_device(X, Xq, scale, sums, dev_info)
     if X.dtype is not torch.bfloat16:
         raise TypeError("X must be bfloat16")
@@ -493,6 +508,12 @@ def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale:
                       dev_info: torch.Tensor, stream=None):
     """quant_tokens of silu(G) * U, an MLP's gated activation, without
     rounding it to bf16 in between (sgpt_quant_tokens_silu)."""
+    if stream is None and _marshal is not None:
+        status = _marshal.quant_tokens_silu(G, U, Xq, scale, sums, dev_info)
+        if status == SGPT_OK:
+            return
+        if status > 0:
+            raise SgptError(status, "sgpt_quant_tokens_silu")
     dev = _one_device(G, U, Xq, scale, sums, dev_info)
     if not (G.dtype is torch.bfloat16 and U.dtype is torch.bfloat16):
         raise TypeError("G and U must be bfloat16")
@@ -510,6 +531,12 @@ def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: 
     """Y = X W^T in 8-bit integers (sgpt_linear_i8): Xq, scale, sums from
     quant_tokens, codes [d_out, d_in] int8 from quant_codes with its grid and
     qbits, Y [n, d_out] fp32 or bf16."""
+    if stream is None and _marshal is not None:
+        status = _marshal.linear_i8(Xq, scale, sums, codes, grid, Y, dev_info, qbits)
+        if status == SGPT_OK:
+            return
+        if status > 0:
+            raise SgptError(status, "sgpt_linear_i8")
     dev = _one_device(Xq, scale, sums, codes, grid, Y, dev_info)
     y_bf16 = Y.dtype is torch.bfloat16
     if not (codes.dtype is torch.int8 and grid.dtype is torch.float32 and (y_bf16 or Y.dtype is torch.float32)):
@@ -543,6 +570,12 @@ def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.
     may be strided, e.g. parts of one q/k/v buffer), offsets [n_seq + 1] int32
     on the device: sequence s has the rows offsets[s]:offsets[s + 1]. scale:
     width ** -0.5 when None."""
+    if stream is None and _marshal is not None:
+        status = _marshal.attention(Q, K, V, offsets, O, dev_info, scale)
+        if status == SGPT_OK:
+            return
+        if status > 0:
+            raise SgptError(status, "sgpt_attention")
     dev = _one_device(Q, K, V, offsets, O, dev_info)
     ldq, ldk, ldv, ldo = _heads_stride(Q, "Q"), _heads_stride(K, "K"), _heads_stride(V, "V"), _heads_stride(O, "O")
     n, heads, width = shape = Q.shape

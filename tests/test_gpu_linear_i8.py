@@ -357,3 +357,54 @@ def test_pruned_and_quantized_layer_runs_as_integers():
     assert torch.equal((grid[:, :1] * ints.float()), W)                  # the fp32 levels themselves
     assert int((ints == 0).sum()) >= d_out * d_in // 2                   # pruned weights are exact zeros
     _check_linear(Y, q.double() @ ints.t(), s, grid)
+
+
+def test_marshalled_calls_are_the_checked_ones(monkeypatch):
+    """The extension module makes the plain calls itself, with the same result
+    as the Python path, and leaves the others to it."""
+    from post_pruning_b200 import sgpt as S
+    pp.lib()
+    m = S._marshal
+    X = torch.randn(5, 2 * 512, device=DEV, generator=_gen(2)).bfloat16()[:, 512:]
+    codes = torch.randint(-128, 128, (70, 512), device=DEV, generator=_gen(3)).to(torch.int8)
+    grid = torch.rand(70, 2, device=DEV, generator=_gen(4))
+    H = torch.randn(9, 6, 64, device=DEV, generator=_gen(5)).bfloat16()
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device=DEV)
+    info = pp.new_info()
+
+    def calls():
+        q, s, t = _tokens(5, 512)
+        Y, O = torch.empty(5, 70, device=DEV), torch.empty(9, 2, 64, device=DEV, dtype=torch.bfloat16)
+        pp.quant_tokens(X, q, s, t, info)
+        pp.linear_i8(q, s, t, codes, grid, Y, info)
+        pp.attention(H[:, :2], H[:, 2:4], H[:, 4:], off, O, info)
+        q2, s2, t2 = _tokens(5, 512)
+        pp.quant_tokens_silu(X, X, q2, s2, t2, info)
+        return q, s, t, Y, O, q2, s2, t2
+
+    fast = calls()
+    monkeypatch.setattr(S, "_marshal", None)
+    for a, b in zip(fast, calls()):
+        assert torch.equal(a, b)
+    monkeypatch.undo()
+    q, s, t = _tokens(5, 512)
+    Y = torch.empty(5, 70, device=DEV)
+    assert m.quant_tokens(X, q, s, t, info) == 0 and m.linear_i8(q, s, t, codes, grid, Y, info, 8) == 0
+    for bad in ((X.float(), q, s, t, info), (X.t(), q, s, t, info), (X, q[:4], s, t, info), (X, q, s.double(), t, info),
+                (X, q, s, t.cpu(), info), (X, q.t().contiguous().t(), s, t, info), (X[:, :500], q, s, t, info)):
+        assert m.quant_tokens(*bad) == -1
+    for bad in (dict(qbits=9), dict(Y=Y.half()), dict(Y=Y[:, :69]), dict(codes=codes[:, :500]), dict(grid=grid[:, 0])):
+        a = dict(codes=codes, grid=grid, Y=Y, qbits=8) | bad
+        assert m.linear_i8(q, s, t, a["codes"], a["grid"], a["Y"], info, a["qbits"]) == -1
+        with pytest.raises((ValueError, TypeError, pp.SgptError)):
+            pp.linear_i8(q, s, t, a["codes"], a["grid"], a["Y"], info, qbits=a["qbits"])
+    # a call that the library refuses comes back with its status
+    with pytest.raises(pp.SgptError):
+        pp.quant_tokens(X[:, :40], *_tokens(5, 40), info)
+    with pytest.raises(pp.SgptError):
+        pp.quant_tokens(X[:1].expand(5, 512), q, s, t, info)
+    side = torch.cuda.Stream()
+    pp.linear_i8(q, s, t, codes, grid, Y, info, stream=side)             # an explicit stream
+    side.synchronize()
+    assert torch.equal(Y, fast[3])
+    pp.raise_on_info(info)

@@ -147,3 +147,22 @@ def test_binding_refuses_before_the_library():
     assert S._row_stride(torch.zeros(1, 64, **f).expand(4, 64), "X") == 0
     assert S._row_stride(torch.zeros(4, 64, **f)[::4], "X") == 64
     assert S._heads_stride(torch.zeros(4, 6, 64, **f)[:, 2:4], "Q") == 6 * 64
+
+
+def test_marshalling_answers_only_what_is_plainly_valid():
+    """The extension module takes no CPU tensor, wrong type or wrong count;
+    the Python functions then raise."""
+    pp.lib()
+    m = S._marshal
+    X, q = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.int8)
+    s, t, info = torch.zeros(4), torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    if torch.cuda.is_available():
+        pytest.skip("the refusals below are those of a machine without a GPU")
+    assert m.quant_tokens(X, q, s, t, info) == -1
+    assert m.quant_tokens(X, q, s, t) == -1
+    assert m.quant_tokens(None, q, s, t, info) == -1
+    assert m.quant_tokens_silu(X, X, q, s, t, info) == -1
+    assert m.linear_i8(q, s, t, q, s, s, info, "8") == -1
+    assert m.attention(X, X, X, t, X, info, None) == -1
+    with pytest.raises(TypeError):
+        m.bind(1, 2, 3)
