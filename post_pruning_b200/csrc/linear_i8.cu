@@ -599,17 +599,57 @@ struct Args {
   cudaStream_t st;
 };
 
-// What the pair kernel takes on tiles of 256 channels x bn tokens with K in
-// `split` parts, in twentieths of a 256 x 256 tile's K stage (about 16 ns):
-// waves of 74 pairs, each of kt / split stages (a stage of a 256 x 128 tile
-// measured 0.7 of a 256 x 256 tile's: 225 and 325 ns), and the adding of the
-// parts (2 to 3 us at bn = 256). K in more than two is not tried: clusters
-// of eight such CTAs do not all find room at once (16 of them took two waves).
-long long pair_cost(int rows, int n, int d, int bn, int split) {
-  const long long items = (long long)cdiv(rows, 2 * kBM) * cdiv(n, bn);
-  const int kt = cdiv(d, kBK), pairs = kNumSMs / 2;
-  if (split > 1 && (items * split > pairs || split > kt)) return INT64_MAX;
-  return cdivll(items * split, pairs) * cdiv(kt, split) * (bn > 128 ? 20 : 14) + (split > 1 ? bn * 2 / 3 : 0);
+// Which kernel, how many tokens a tile, K in how many parts: the least of the
+// times (us) that these lines, fitted to every variant on eight layers (768 to
+// 25600 wide) with 1 to 2000 tokens, expect; over those the choice was 1.3 %
+// off the best one. One token of 768 -> 768 took 4.3 us in clusters of three
+// and takes 2.9 in single CTAs, 333 tokens 6.1 in pairs and 3.4.
+//   The split kernel: a wave of 296 CTAs costs its start and epilogue, and
+// each K stage its time in every layer of 148 CTAs (two on an SM share it);
+// adding K's parts up costs a cluster's two barriers and grows with its size.
+// The pair kernel: waves of 74 pairs; K in more than two is not tried there:
+// clusters of eight such CTAs do not all find room at once (16 of them took
+// two waves); clusters of seven CTAs of the split kernel did not either.
+//   Codes that the L2 does not hold come at 6 TB/s, and at 60 GB/s a CTA.
+struct Plan {
+  bool pair;
+  int bn, split;
+};
+struct PlanLine {
+  bool pair;
+  int bn;
+  float start, wave, stage, split, part;
+};
+constexpr PlanLine kPlanLines[] = {{false, 16, 0.f, 2.6f, 0.13f, 1.0f, 0.46f},  {false, 32, 0.f, 2.8f, 0.147f, 0.7f, 0.6f},
+                                   {false, 64, 0.f, 3.3f, 0.19f, 0.76f, 0.51f}, {true, 128, 2.0f, 2.8f, 0.175f, 2.1f, 0.f},
+                                   {true, 256, 0.5f, 5.0f, 0.303f, 2.3f, 0.f}};
+
+Plan plan(int rows, int n, int d) {
+  const int kt = cdiv(d, kBK);
+  const float codes = (float)rows * (float)d;
+  Plan best{true, 256, 1};
+  float least = INFINITY;
+  for (const PlanLine& l : kPlanLines) {
+    const long long tiles = (long long)cdiv(rows, l.pair ? 2 * kBM : kBM) * cdiv(n, l.bn);
+    const long long room = l.pair ? kNumSMs / 2 : kSplitPerSM * kNumSMs;      // clusters of a part each
+    if (!l.pair && tiles > 64 * room) continue;
+    for (int split = 1; split <= (l.pair ? 2 : kMaxSplit) && split <= kt; split *= 2) {
+      if (split > 1 && tiles * split > room) break;
+      const long long units = tiles * split, waves = cdivll(units, room), rest = units - (waves - 1) * room;
+      const long long layers = l.pair ? waves : 2 * (waves - 1) + (rest > kNumSMs ? 2 : 1);
+      float t = l.start + l.wave * waves + l.stage * layers * cdiv(kt, split);
+      if (split > 1) t += l.split + l.part * (split - 1);
+      if (codes > 32e6f) {
+        const float ctas = (float)std::min(units, room) * (l.pair ? 2 : 1);
+        t = std::max(t, 3.f + codes / std::min(6.0e6f, ctas * 6.0e4f));
+      }
+      if (t < least) {
+        least = t;
+        best = Plan{l.pair, l.bn, split};
+      }
+    }
+  }
+  return best;
 }
 
 template <int BN, class T>
@@ -630,7 +670,7 @@ cudaError_t launch_pair(const Args& a, int split) {
 }
 
 template <int BN, class T>
-cudaError_t launch_split(const Args& a) {
+cudaError_t launch_split(const Args& a, int split) {
   CUtensorMap wm, xm;
   if (!map_i8(&wm, a.codes, a.out.rows, a.d, kBM) || !map_i8(&xm, a.Xq, a.out.n, a.d, BN)) return cudaErrorInvalidValue;
   static PerDevice attrs;
@@ -640,12 +680,6 @@ cudaError_t launch_split(const Args& a) {
   });
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)cdiv(a.out.rows, kBM) * cdiv(a.out.n, BN);
-  const int kt = cdiv(a.d, kBK);
-  // parts of K: as many as find room on the GPU together (a power of two:
-  // clusters of seven took a third longer than clusters of four), of two
-  // stages at least
-  int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= (long long)kNumSMs * kSplitPerSM && split * 2 <= kt) split *= 2;
   if (tiles * split > INT32_MAX) return cudaErrorInvalidValue;
   return launch_after(linear_i8_split_kernel<BN, T>, (unsigned)(tiles * split), kThreads, split_smem(BN), split, a.st, wm,
                       xm, a.d, split, a.out, a.info, wait_limit_cycles());
@@ -653,22 +687,10 @@ cudaError_t launch_split(const Args& a) {
 
 template <class T>
 cudaError_t dispatch(const Args& a) {
-  const int n = a.out.n;
-  if (n <= 16) return launch_split<16, T>(a);
-  if (n <= 32) return launch_split<32, T>(a);
-  if (n <= 64) return launch_split<64, T>(a);
-  long long best = INT64_MAX;
-  int bn = 128, split = 1;
-  for (const int b : {256, 128})
-    for (const int p : {1, 2}) {
-      const long long c = pair_cost(a.out.rows, n, a.d, b, p);
-      if ((b == 128 || n > 128) && c < best) {
-        best = c;
-        bn = b;
-        split = p;
-      }
-    }
-  return bn == 256 ? launch_pair<256, T>(a, split) : launch_pair<128, T>(a, split);
+  const Plan p = plan(a.out.rows, a.out.n, a.d);
+  if (p.pair) return p.bn == 256 ? launch_pair<256, T>(a, p.split) : launch_pair<128, T>(a, p.split);
+  return p.bn == 16 ? launch_split<16, T>(a, p.split)
+                    : p.bn == 32 ? launch_split<32, T>(a, p.split) : launch_split<64, T>(a, p.split);
 }
 
 }  // namespace

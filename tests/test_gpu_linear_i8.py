@@ -229,6 +229,24 @@ def test_linear_i8(n, d_in, d_out, dtype):
     assert bool((buf[n:] == -3).all())
 
 
+# one shape for every tile and number of parts of K that the plan can choose
+VARIANTS = [(3, 160, 177), (7, 3232, 110), (2, 4416, 115), (1, 16736, 103), (506, 160, 521), (608, 3552, 130),
+            (321, 5440, 171), (146, 28832, 130), (429, 128, 2740), (599, 4672, 386), (602, 7904, 129), (330, 24544, 130),
+            (460, 128, 11952), (65, 4704, 6305), (216, 128, 10599), (134, 16640, 4707)]
+
+
+@pytest.mark.parametrize("n,d_in,d_out", VARIANTS)
+def test_linear_i8_every_variant(n, d_in, d_out):
+    q, s, t, codes, grid, whole = _problem(n, d_in, d_out, seed=3)
+    info = pp.new_info()
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((n + 2, d_out), -3.0, device=DEV, dtype=dtype)
+        pp.linear_i8(q, s, t, codes, grid, buf[:n], info)
+        pp.raise_on_info(info)
+        _check_linear(buf[:n], whole, s, grid)
+        assert bool((buf[n:] == -3).all())
+
+
 @pytest.mark.parametrize("n", [1, 24, 200])
 def test_linear_i8_many_tiles_per_cta(n):
     q, s, t, codes, grid, whole = _problem(n, 256, 60000)
@@ -295,11 +313,12 @@ def test_results_repeat_and_capture():
         assert torch.equal(bufs[0][3], want[i])
 
 
-def test_linear_i8_wait_times_out():
+@pytest.mark.parametrize("n,d_in,d_out", [(600, 2048, 640), (2, 4416, 115), (65, 4704, 6305), (216, 512, 10599)])
+def test_linear_i8_wait_times_out(n, d_in, d_out):
     """A wait that runs out is reported, leaves the GPU usable, and the same
-    call succeeds again."""
-    q, s, t, codes, grid, whole = _problem(600, 2048, 640)
-    Y = torch.empty(600, 640, device=DEV)
+    call succeeds again: single CTAs, a cluster, pairs, pairs with K in two."""
+    q, s, t, codes, grid, whole = _problem(n, d_in, d_out)
+    Y = torch.empty(n, d_out, device=DEV)
     info = pp.new_info()
     pp.set_wait_limit(1)
     try:
