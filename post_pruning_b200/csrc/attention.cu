@@ -307,12 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   }
   let_next_start();
   after_previous();
-  if (blockIdx.x == 0) {                         // every offset is checked once
-    bool bad = false;
-    for (int b = threadIdx.x; b < sh.n_seq; b += kThreads) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
-    if (__syncthreads_or(bad) && threadIdx.x == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
-  }
-  if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+  Search at_seq;
+  Work w0{0, 0, 0, 0};                           // warp 8's first unit: its offsets load under the set-up
+  if (warp == 8) w0 = find_work(sh, cu, blockIdx.x, lane, at_seq);
+  if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -326,11 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       int index = blockIdx.x;
       uint32_t g = 0, units = 0, groups = 0;     // ring slots, units and groups of slots so far
       uint32_t q_used[2] = {0, 0};
-      bool ok = true, asked = false;
+      bool ok = true, asked = false, first = true;
       Phase answers;
-      Search at_seq;
       while (ok) {
-        const Work w = index < 0 ? Work{0, 0, 0, 0} : find_work(sh, cu, index, lane, at_seq);
+        const Work w = index < 0 ? Work{0, 0, 0, 0} : first ? w0 : find_work(sh, cu, index, lane, at_seq);
+        first = false;
         if (index >= 0) {
           if (lane == 0) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the last answer has been read
@@ -498,6 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         g += 2 * nb;
       }
+    } else if (blockIdx.x == 0) {
+      // every offset is looked at once
+      bool bad = false;
+      for (int b = lane; b < sh.n_seq; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
+      if (__any_sync(0xffffffffu, bad) && lane == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -542,10 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         top = max32(s[3], max32(s[2], top));
         // The first half of the weights is formed with the maximum that the
         // row had before this block, under the search for the block's own;
-        // they are formed again in the rare block that moves the maximum.
+        // they are formed again in the rare block that moves the maximum (the
+        // first block has no maximum before it).
         uint32_t p[32];
         uint64_t sum[2];
-        weights(s[0], s[1], c2, m * sh.c, p, sum);
+        if (j > 0) weights(s[0], s[1], c2, m * sh.c, p, sum);
         const bool grow = j == 0 || (top - m) * sh.c > kGrow;
         if (__any_sync(0xffffffffu, grow)) {
           const float mnew = grow ? top : m;
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   fence_before();
   __syncthreads();
   if (failed && threadIdx.x == 0) set_info(info, SGPT_INFO_TIMEOUT);
-  if (warp == 8) tmem_free(tmem, kTmemCols);
+  if (warp == 9) tmem_free(tmem, kTmemCols);
 }
 
 // bf16 [rows x heads x D], row stride ld elements: boxes of 64 columns of one
