@@ -370,8 +370,8 @@ sgpt_status sgpt_quant_codes(const float* W, int d_out, int d_in, int ldw, const
  *   scale[t] = max_k |X[t][k]| / 127,  Xq[t][k] = rint(127 X[t][k] / max),
  * ties to even, and sums[t] = sum_k Xq[t][k]. The division is IEEE fp32; for
  * bf16 X the codes are the exact ones. A row of zeros has scale 0. A row with
- * a NaN or an infinity sets SGPT_INFO_NONFINITE (and gets codes 0, scale
- * NaN). 0 <= n <= 2^30; n == 0 launches nothing. Inputs and outputs must not
+ * a NaN or an infinity gets codes 0 and scale NaN and sets
+ * SGPT_INFO_NONFINITE (the other rows are then unspecified). 0 <= n <= 2^30; n == 0 launches nothing. Inputs and outputs must not
  * overlap. */
 sgpt_status sgpt_quant_tokens(const uint16_t* X, int64_t n, int d, int64_t ldx, int8_t* Xq, float* scale,
                               int32_t* sums, int* dev_info, void* stream);

@@ -71,7 +71,7 @@ __device__ __forceinline__ void gated8(const uint4& graw, const uint4& uraw, flo
 
 // What a row's codes need of its largest magnitude (given by its bits).
 struct RowScale {
-  float a, k, den, inv;          // code of x = rint(x k / den), inv = 1 / den
+  float a, pre, k, den, inv;     // code of x = rint(x k / den), k = 127 pre, den = a pre, inv = 1 / den
   bool finite, some;             // all values are numbers; one is not zero
 };
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
@@ -81,9 +81,9 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   r.a = __uint_as_float(top);
   // 127 a and 1 / a stay numbers: rows above 2^119 are scaled by 2^-8, rows
   // below 2^-100 by 2^64, exactly (what the first flushes is far below half a code)
-  const float pre = r.a > 0x1p119f ? 0x1p-8f : r.a < 0x1p-100f ? 0x1p64f : 1.f;
-  r.k = 127.f * pre;
-  r.den = r.a * pre;
+  r.pre = r.a > 0x1p119f ? 0x1p-8f : r.a < 0x1p-100f ? 0x1p64f : 1.f;
+  r.k = 127.f * r.pre;
+  r.den = r.a * r.pre;
   r.inv = r.some ? __frcp_rn(r.den) : 0.f;
   return r;
 }
@@ -97,11 +97,19 @@ __device__ __forceinline__ uint2 pack8(const int (&c)[8], int& sum) {
 }
 __device__ __forceinline__ uint2 gated_codes(const float* z, const RowScale& r, int& sum) {
   if (!r.some) return make_uint2(0, 0);
-  const float ratio = r.k * r.inv;
+  const float ratio = 127.f * r.inv;
   int c[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) c[j] = __float_as_int(fmaf(z[j], ratio, kRound));
   return pack8(c, sum);
+}
+// The row's gated values as gated_codes() takes them, times pre.
+template <int N>
+__device__ __forceinline__ void prescale(float (&z)[N], const RowScale& r) {
+  if (r.pre != 1.f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] *= r.pre;
+  }
 }
 __device__ __forceinline__ uint2 exact_codes(const uint4& raw, const RowScale& r, int& sum) {
   if (!r.some) return make_uint2(0, 0);
@@ -203,6 +211,7 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
     return;
   }
   const RowScale rs = row_scale(top);
+  if constexpr (GATED) prescale(z, rs);
   int sum = 0;
   uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
 #pragma unroll
@@ -228,11 +237,12 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
   if (t == 0 && part == 0) finish_row(rs, sum, scale + row, sums + row, info);
 }
 
-// The gated rows above 8192 elements, when there are many. A row takes 4 bytes
-// per element in and more arithmetic than a CTA can hide behind its own loads
-// (with a row per CTA of 512 threads, 4099 x 25600 took 161 us, 3.3 TB/s):
-// persistent CTAs of 512 keep two rows of G and U in shared memory, one
-// copied in (bulk copies) while the other is quantized.
+// The gated rows above 16384 elements, when there are many. A row takes 4
+// bytes per element in and more arithmetic than a CTA can hide behind its own
+// loads: persistent CTAs of 512 keep two rows of G and U in shared memory, one
+// copied in (bulk copies) while the other is quantized (4099 x 25600: 98 us,
+// 5.4 TB/s; with a row per CTA 161 us). Shorter rows are quicker with several
+// CTAs an SM (4096 x 11008: 59 us and 97).
 constexpr int kGatedThreads = 512, kGatedVec = 7;
 constexpr int kGatedMax = 28672;                                     // elements: two rows fill the shared memory
 static_assert(kGatedMax <= kGatedThreads * kGatedVec * 8, "a row in registers");
@@ -302,6 +312,7 @@ __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
       load(later, b);
     }
     const RowScale rs = row_scale(top);
+    prescale(z, rs);
     int sum = 0;
     uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
 #pragma unroll

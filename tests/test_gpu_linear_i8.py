@@ -148,6 +148,28 @@ def test_quant_tokens_silu(n, d, strided):
     assert torch.equal(t.long(), q.long().sum(1))
 
 
+@pytest.mark.parametrize("d", [96, 512 * 56])                # a row per warp; rows in shared memory
+@pytest.mark.parametrize("size", [1e-37, 3e-38, 1e-30, 1e-25, 1e30, 3e38])
+def test_quant_tokens_silu_extremes(d, size):
+    """Rows whose gated values are all tiny or huge: 127 / max and 127 z stay
+    inside fp32. (Values this small are short of bits in fp32: the codes are
+    checked against the fp32 values u, where silu(g) is 1 to the last bit.)"""
+    g = _gen(d)
+    n = 70
+    G = torch.full((n, d), 64.0, device=DEV).bfloat16()               # silu(64) = 64
+    U = ((torch.rand(n, d, device=DEV, generator=g) * 2 - 1) * (size / 64)).bfloat16()
+    q, s, t = _tokens(n, d)
+    info = pp.new_info()
+    pp.quant_tokens_silu(G, U, q, s, t, info)
+    pp.raise_on_info(info)
+    z = U.double() * 64
+    top = z.abs().amax(1)
+    off = (q.double() - 127 * z / top[:, None]).abs()
+    assert float(off.max()) <= 0.5 + 127 * (2 * Z_REL + 2 * 2.0 ** -24)
+    assert bool(((s.double() - top / 127).abs() <= Z_REL * top / 127 + 2.0 ** -149).all())
+    assert torch.equal(t.long(), q.long().sum(1))
+
+
 @pytest.mark.parametrize("qbits", [2, 4, 8])
 def test_quant_codes_stand_for_the_grid(qbits):
     """Codes of arbitrary weights are the nearest levels, and codes of weights
