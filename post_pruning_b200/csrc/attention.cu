@@ -43,8 +43,8 @@ using namespace ptx;
 
 constexpr int kT = 128;                         // query rows per tile, keys per block
 constexpr int kThreads = 384;                   // 2 x 4 softmax warps, TMA, MMA, two idle
-// registers a thread after the split: 2 x 216 + 72 = 3 x 168, what the block is launched with
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// registers a thread after the split: 2 x 200 + 104 = 3 x 168, what the block is launched with
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr int kBox = kT * 128;                  // 16 KB: 128 rows x 64 bf16
 constexpr int kFree = 8;                        // barriers that free ring slots, more than ring slots
 constexpr float kGrow = 8.f;                    // exponent growth that moves the running maximum
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         };
         auto units_done = [&]() -> bool {                  // false: a wait ran out
           uint32_t g = 0, groups = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, vn = 0;
+          bool ahead = false;                              // the first tile's first scores are under way
           for (uint32_t u = 0;; ++u) {
             if (!mbar_wait(wfull + 8 * (u & 1), (u >> 1) & 1, wait_cycles)) return false;
             const Work w = work[u & 1];
@@ -429,11 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int mine = h ? nb1 : nb0;
-              if (!mine) continue;
+              if (!mine || (h == 0 && ahead)) continue;
               if (!mbar_wait(qfull + 8 * h, qn[h]++ & 1, wait_cycles)) return false;
               score(h, g, mine == 1);
             }
+            ahead = false;
             mma_commit(free0 + 8 * (groups++ % kFree));
+            const uint32_t next = g + 2 * nb;              // the next unit's first ring slot
             for (int j = 0; j < nb; ++j) {
               const uint32_t gv = ++g;
               if (!loaded(gv)) return false;
@@ -461,6 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                   score(h, g, j + 2 == mine);
                 } else {
                   mma_commit(ofull + 8 * h);
+                  // the first tile goes on to the next unit, if that is here,
+                  // while the second one is still at this unit's last block
+                  const uint32_t v = (u + 1) & 1;
+                  if (h == 0 && mbar_test(wfull + 8 * v, ((u + 1) >> 1) & 1) && work[v].len &&
+                      mbar_test(full0 + 8 * (next % kStages), (next / kStages) & 1) && mbar_test(qfull, qn[0] & 1)) {
+                    ++qn[0];
+                    score(0, next, work[v].blocks(sh, 0) == 1);
+                    ahead = true;
+                  }
                 }
               }
               mma_commit(free0 + 8 * (groups++ % kFree));
