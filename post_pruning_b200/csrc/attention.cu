@@ -417,7 +417,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (last) mma_commit(qempty + 8 * h);
         };
         auto units_done = [&]() -> bool {                  // false: a wait ran out
-          uint32_t g = 0, groups = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, vn = 0;
+          uint32_t g = 0, groups = 0;
+          // parities of the next waits on qfull, pfull (per tile) and vready
+          uint32_t parities = 0;
+          constexpr uint32_t kQ = 1, kP = 4, kV = 16;
+          auto next_of = [&](uint32_t bit) {
+            const uint32_t p = (parities & bit) != 0;
+            parities ^= bit;
+            return p;
+          };
           bool ahead = false;                              // the first tile's first scores are under way
           for (uint32_t u = 0;; ++u) {
             if (!mbar_wait(wfull + 8 * (u & 1), (u >> 1) & 1, wait_cycles)) return false;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             for (int h = 0; h < 2; ++h) {
               const int mine = h ? nb1 : nb0;
               if (!mine || (h == 0 && ahead)) continue;
-              if (!mbar_wait(qfull + 8 * h, qn[h]++ & 1, wait_cycles)) return false;
+              if (!mbar_wait(qfull + 8 * h, next_of(kQ << h), wait_cycles)) return false;
               score(h, g, mine == 1);
             }
             ahead = false;
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
               if (!loaded(gv)) return false;
               if (j == tail) {
                 mbar_arrive(vask);
-                if (!mbar_wait(vready, vn++ & 1, wait_cycles)) return false;
+                if (!mbar_wait(vready, next_of(kV), wait_cycles)) return false;
               }
               const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
               ++g;                                         // the next block's K
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
               for (int h = 0; h < 2; ++h) {
                 const int mine = h ? nb1 : nb0;
                 if (j >= mine) continue;
-                const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT, par = pn[h]++ & 1;
+                const uint32_t acc = tmem + 2 * kT + h * kT, pd = tmem + h * kT, par = next_of(kP << h);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                   if (!mbar_wait(pfull + 16 * h + 8 * half, par, wait_cycles)) return false;
@@ -468,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                   // while the second one is still at this unit's last block
                   const uint32_t v = (u + 1) & 1;
                   if (h == 0 && mbar_test(wfull + 8 * v, ((u + 1) >> 1) & 1) && work[v].len &&
-                      mbar_test(full0 + 8 * (next % kStages), (next / kStages) & 1) && mbar_test(qfull, qn[0] & 1)) {
-                    ++qn[0];
+                      mbar_test(full0 + 8 * (next % kStages), (next / kStages) & 1) && mbar_test(qfull, parities & kQ)) {
+                    parities ^= kQ;
                     score(0, next, work[v].blocks(sh, 0) == 1);
                     ahead = true;
                   }
