@@ -404,9 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         const uint64_t q_desc = sw128_desc(s0), k_desc = sw128_desc(ring), v_desc = sw128_desc(ring, kBox);
         // No instruction more than needed between the products: the tensor
         // cores idle while this thread is late.
-        auto loaded = [&](uint32_t x) { return mbar_wait(full0 + 8 * (x % kStages), (x / kStages) & 1, wait_cycles); };
-        auto score = [&](int h, uint32_t x, bool last) {   // S_h = Q_h K^T
-          const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)((x % kStages) * kTile >> 4);
+        struct Slot {                                      // of the ring, in the order of use
+          uint32_t s, parity;
+          __device__ void step() {
+            if (++s == kStages) {
+              s = 0;
+              parity ^= 1;
+            }
+          }
+        };
+        auto loaded = [&](Slot x) { return mbar_wait(full0 + 8 * x.s, x.parity, wait_cycles); };
+        auto is_loaded = [&](Slot x) { return mbar_test(full0 + 8 * x.s, x.parity); };
+        auto score = [&](int h, Slot x, bool last) {       // S_h = Q_h K^T
+          const uint64_t qd = q_desc + (uint64_t)(h * kTile >> 4), kd = k_desc + (uint64_t)(x.s * (kTile >> 4));
           const uint32_t acc = tmem + h * kT;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -417,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (last) mma_commit(qempty + 8 * h);
         };
         auto units_done = [&]() -> bool {                  // false: a wait ran out
-          uint32_t g = 0, groups = 0;
+          Slot at{0, 0};                                   // the next slot to use
+          uint32_t groups = 0;
           // parities of the next waits on qfull, pfull (per tile) and vready
           uint32_t parities = 0;
           constexpr uint32_t kQ = 1, kP = 4, kV = 16;
@@ -434,26 +445,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             if (!w.len) return true;
             const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
             const int tail = w.len % kT ? w.len / kT : nb; // the block inside which the sequence ends
-            if (!loaded(g)) return false;
+            if (!loaded(at)) return false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int mine = h ? nb1 : nb0;
               if (!mine || (h == 0 && ahead)) continue;
               if (!mbar_wait(qfull + 8 * h, next_of(kQ << h), wait_cycles)) return false;
-              score(h, g, mine == 1);
+              score(h, at, mine == 1);
             }
             ahead = false;
             mma_commit(free0 + 8 * (groups++ % kFree));
-            const uint32_t next = g + 2 * nb;              // the next unit's first ring slot
+            at.step();
+            bool v_here = false, k_here = false;           // this block's V and the next one's K have been seen
             for (int j = 0; j < nb; ++j) {
-              const uint32_t gv = ++g;
-              if (!loaded(gv)) return false;
+              if (!v_here && !loaded(at)) return false;
               if (j == tail) {
                 mbar_arrive(vask);
                 if (!mbar_wait(vready, next_of(kV), wait_cycles)) return false;
               }
-              const uint64_t vd = v_desc + (uint64_t)((gv % kStages) * kTile >> 4);
-              ++g;                                         // the next block's K
+              const uint64_t vd = v_desc + (uint64_t)(at.s * (kTile >> 4));
+              at.step();
+              const Slot k = at;                           // the next block's K (or the next unit's)
+              v_here = false;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int mine = h ? nb1 : nb0;
@@ -466,24 +479,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
 #pragma unroll
                   for (int x = 4 * half; x < 4 * half + 4; ++x)
                     mma_ts(acc, pd + 8 * x, vd + (uint64_t)(2048 * x >> 4), idesc(D, true), x > 0 ? 1u : (uint32_t)(j > 0));
+                  if (half == 0 && j + 1 < nb) {
+                    // looked for here, where there is time until the second half
+                    if (h == 0) {
+                      k_here = is_loaded(k);
+                    } else {
+                      Slot v = k;
+                      v.step();
+                      v_here = is_loaded(v);
+                    }
+                  }
                 }
                 if (j + 1 < mine) {
-                  if (!loaded(g)) return false;
-                  score(h, g, j + 2 == mine);
+                  if (!k_here && !loaded(k)) return false;
+                  k_here = true;
+                  score(h, k, j + 2 == mine);
                 } else {
                   mma_commit(ofull + 8 * h);
                   // the first tile goes on to the next unit, if that is here,
                   // while the second one is still at this unit's last block
-                  const uint32_t v = (u + 1) & 1;
-                  if (h == 0 && mbar_test(wfull + 8 * v, ((u + 1) >> 1) & 1) && work[v].len &&
-                      mbar_test(full0 + 8 * (next % kStages), (next / kStages) & 1) && mbar_test(qfull, parities & kQ)) {
-                    parities ^= kQ;
-                    score(0, next, work[v].blocks(sh, 0) == 1);
-                    ahead = true;
+                  if (h == 0) {
+                    Slot first = k;                        // of the next unit
+                    if (nb1 > nb0) {
+                      first.step();
+                      first.step();
+                    }
+                    const uint32_t v = (u + 1) & 1;
+                    if (mbar_test(wfull + 8 * v, ((u + 1) >> 1) & 1) && work[v].len && is_loaded(first) &&
+                        mbar_test(qfull, parities & kQ)) {
+                      parities ^= kQ;
+                      score(0, first, work[v].blocks(sh, 0) == 1);
+                      ahead = true;
+                    }
                   }
                 }
               }
               mma_commit(free0 + 8 * (groups++ % kFree));
+              if (j + 1 < nb) at.step();
+              k_here = false;
             }
           }
         };
