@@ -15,8 +15,11 @@
 //
 // Two kernels, both warp-specialized: warp 0 feeds a ring of 128-byte K
 // stages by TMA (128-byte swizzle, out of range reads give zero codes), warp 1
-// issues four MMAs (K = 32) per stage, warps 2-5 are the epilogue. Every wait
-// is bounded as everywhere in this library.
+// issues four MMAs (K = 32) per stage, the others are the epilogue: four in the
+// split kernel, eight (two for the columns of each TMEM quarter) in the pair
+// kernel, where K is short and the epilogue not hidden: 256 -> 3080 with 3553
+// tokens in 16.0 us, 18.8 with four; 25600 wide either takes the same. Every
+// wait is bounded as everywhere in this library.
 //
 // linear_i8_pair_kernel, many tiles: persistent CTA pairs (cta_group::2) on
 // tiles of 256 channels x 256 (or 128) tokens, each CTA with half of the rows of both
@@ -157,18 +160,18 @@ __device__ __forceinline__ void store4(uint16_t* y, const float (&v)[4]) {
 }
 
 // The split sums: every CTA of the cluster holds its part of a tile, token by
-// token, at `part` ([tokens][128] int32); this one's epilogue warps (w of 4)
+// token, at `part` ([tokens][128] int32); this one's epilogue warps (w of WARPS)
 // add up and write every `split`-th token. first + step * p: the CTA of part
 // p. A lane takes four channels: 16 bytes of distributed shared memory at a
 // time, 16 loads in flight, are what keeps this short.
-template <class T>
+template <class T, int WARPS>
 __device__ __forceinline__ void add_parts(uint32_t part, int split, int sp, int first, int step, int w, int lane,
                                           int row0, int n0, int cols, const Out& out, const Channel (&ch)[4],
                                           const float* tok_scale, const int32_t* tok_sum) {
   const int rows = out.rows, row = row0 + 4 * lane;
   const bool whole = rows % 4 == 0 && row + 3 < rows;
   T* Y = static_cast<T*>(out.Y) + (long long)n0 * rows + row;
-  const int every = 4 * split;
+  const int every = WARPS * split;
   for (int c0 = sp + split * w; c0 < cols; c0 += 4 * every) {
     int4 acc[4] = {};
     float ts[4];
@@ -220,13 +223,14 @@ __host__ __device__ constexpr int pair_stages(int bn) { return bn > 128 ? 6 : 8;
 __host__ __device__ constexpr size_t pair_smem(int bn) {
   return (size_t)pair_stages(bn) * pair_stage(bn) + 1024 + 256 + 2 * 8 * bn;
 }
+constexpr int kPairThreads = 320;               // producer, MMA, 8 epilogue warps
 constexpr int kGroupRows = 8;                   // 256-channel tile rows walked together
 
 template <int BN, class T>
-__global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                                     const __grid_constant__ CUtensorMap xmap, int d,
-                                                                     int split, const Out out, int* info,
-                                                                     const long long wait_cycles) {
+__global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                         const __grid_constant__ CUtensorMap xmap, int d,
+                                                                         int split, const Out out, int* info,
+                                                                         const long long wait_cycles) {
   constexpr int kStages = pair_stages(BN), kStage = pair_stage(BN);
   static_assert(BN * kBM * 4 <= kStages * kStage, "the parts of a split sum fit the ring");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 8);            // used in the pair's first CTA: four warps of each
+      mbar_init(tempty0 + 8 * b, 16);           // used in the pair's first CTA: eight warps of each
     }
     mbar_init(mdone, 1);
     mbar_init_fence();
@@ -343,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
       if (!mbar_wait(mdone, 0, kDrainCycles)) failed = 1;
     }
   } else {
-    const int q = warp & 3, et = threadIdx.x - 64;       // TMEM lanes 32 q .. of this warp; epilogue thread
+    // TMEM lanes 32 q .. of this warp, and its half of the columns; epilogue thread
+    const int q = warp & 3, part_of = (warp - 2) >> 2, et = threadIdx.x - 64;
     const uint32_t leader_tempty0 = map_rank(tempty0, leader);
     int u = 0;
     for (long long w = first_item; w < items; w += step, ++u) {
@@ -351,13 +356,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
       decode(w, mt, nt);
       const int b = u & 1, n0 = nt * BN, row = mt * 2 * kBM + (int)half * kBM + q * 32 + lane;
       const int cols = min(BN, n - n0);
-      for (int e = et; e < BN; e += 128) {
+      for (int e = et; e < BN; e += 256) {
         const bool in = e < cols;
         tok_scale[b * BN + e] = in ? out.xs[n0 + e] : 0.f;
         tok_sum[b * BN + e] = in ? out.xsum[n0 + e] : 0;
       }
       const Channel ch = channel(out, row);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       int bad = failed;
       if (!bad) bad = !mbar_wait(tfull0 + 8 * b, (u >> 1) & 1, wait_cycles);
       bad = __any_sync(0xffffffffu, bad);      // one decision per warp: the TMEM loads are warp-collective
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
         int32_t* part = reinterpret_cast<int32_t*>(smem) + q * 32 + lane;
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
+        for (int c = part_of * (BN / 2); c < min(cols, (part_of + 1) * (BN / 2)); c += 32) {
           uint32_t v[2][16];
           tmem_ld16(acc + c, v[0]);
           tmem_ld16(acc + c + 16, v[1]);
@@ -406,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_i8_pair_kernel(const __gri
     bool all = write;
     for (int p = 0; p < 2 * split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
     if (warp >= 2 && all)
-      add_parts<T>(s0, split, sp, (int)half, 2, warp - 2, lane, row0, nt * BN, min(BN, n - nt * BN), out, ch4, tok_scale,
-                   tok_sum);
+      add_parts<T, 8>(s0, split, sp, (int)half, 2, warp - 2, lane, row0, nt * BN, min(BN, n - nt * BN), out, ch4,
+                      tok_scale, tok_sum);
   }
   __syncwarp();
   fence_before();
@@ -573,7 +578,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
     cluster_sync();
     bool all = write;
     for (int p = 0; p < split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
-    if (warp >= 2 && all) add_parts<T>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, ch4, tok_scale, tok_sum);
+    if (warp >= 2 && all)
+      add_parts<T, 4>(s0, split, rank, 0, 1, warp - 2, lane, mt * kBM, n0, cols, out, ch4, tok_scale, tok_sum);
     cluster_sync();                                        // no CTA leaves while its sums are read
   }
   fence_before();
@@ -670,7 +676,7 @@ cudaError_t launch_pair(const Args& a, int split) {
   if (e != cudaSuccess) return e;
   const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, BN);
   const int pairs = split > 1 ? (int)items * split : (int)std::min<long long>(items, kNumSMs / 2);
-  return launch_after(linear_i8_pair_kernel<BN, T>, 2 * pairs, kThreads, pair_smem(BN), 2 * split, a.st, wm, xm, a.d,
+  return launch_after(linear_i8_pair_kernel<BN, T>, 2 * pairs, kPairThreads, pair_smem(BN), 2 * split, a.st, wm, xm, a.d,
                       split, a.out, a.info, wait_limit_cycles());
 }
 
