@@ -413,7 +413,10 @@ sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* 
  * product in bf16; O is rounded once. Values in masked places (later rows,
  * other sequences, rows outside) never reach a row's result as long as the
  * row's own sequence is finite; a result that is not finite sets
- * SGPT_INFO_NONFINITE. O must not overlap Q, K or V. */
+ * SGPT_INFO_NONFINITE. O must not overlap Q, K or V. The same call gives the
+ * same bits; n_tok, n_seq and the head counts decide whether the sums of a
+ * row are formed in one or in several parts, so the same sequence packed with
+ * others may differ in its last rounding. */
 sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
                            int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
                            int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream);

@@ -23,6 +23,12 @@
 // up to 1); then the warp rescales its rows of O in TMEM itself: S of block j
 // is complete only after the product of block j - 1.
 //
+// Few units (few heads, long sequences) leave SMs idle: there a cluster of 2, 4
+// or 8 CTAs shares a unit, each with a part of its keys and a maximum, sum
+// and O of its own, which are joined through distributed shared memory: each
+// CTA writes its share of the rows, O = sum_p f_p O_p / sum_p f_p l_p with
+// f_p = exp(m_p - max m). Those CTAs take one unit only.
+//
 // Masked places never reach a result: scores after the diagonal are replaced
 // by -inf whatever they are, and rows of V after the end of the sequence are
 // zeroed in shared memory before the product that would read them. Rows
@@ -165,7 +171,17 @@ struct Work {
   __device__ int head(const Shape& sh, int h) const { return sh.pair ? 2 * head_unit + h : head_unit; }
   // tile h's first row in the sequence, and its key blocks
   __device__ int row(const Shape& sh, int h) const { return sh.pair ? unit * kT : (2 * unit + h) * kT; }
-  __device__ int blocks(const Shape& sh, int h) const { return row(sh, h) < len ? row(sh, h) / kT + 1 : 0; }
+  __device__ int all_blocks(const Shape& sh, int h) const { return row(sh, h) < len ? row(sh, h) / kT + 1 : 0; }
+  // of these, the ones of CTA `part` of the unit's cluster, from first_block on
+  template <int PARTS>
+  __device__ int first_block(const Shape& sh, int part) const {
+    return PARTS > 1 ? max(all_blocks(sh, 0), all_blocks(sh, 1)) * part / PARTS : 0;
+  }
+  template <int PARTS>
+  __device__ int blocks(const Shape& sh, int h, int part) const {
+    if (PARTS == 1) return all_blocks(sh, h);
+    return max(0, min(all_blocks(sh, h), first_block<PARTS>(sh, part + 1)) - first_block<PARTS>(sh, part));
+  }
 };
 
 // Where the last search ended: the first of 32 sequences, and the units before it.
@@ -258,12 +274,13 @@ struct Phase {
   __device__ uint32_t next() { return n++ & 1u; }
 };
 
-template <int D>
+template <int D, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap, const int32_t* __restrict__ cu, const Shape sh,
     uint16_t* __restrict__ O, int* info, const long long wait_cycles) {
   constexpr int kTile = tile_bytes(D), kStages = stages_for(D);
+  constexpr bool SPLIT = PARTS > 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -274,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   __shared__ Work work[2];
   __shared__ int group_of[kStages];              // producer's: what frees each ring slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = SPLIT ? (int)cluster_rank() : 0;
   const uint32_t s0 = smem_u32(smem);
   const uint32_t ring = s0 + 2 * kTile;
   // [2]: one per tile or per work slot
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   after_previous();
   Search at_seq;
   Work w0{0, 0, 0, 0};                           // warp 8's first unit: its offsets load under the set-up
-  if (warp == 8) w0 = find_work(sh, cu, blockIdx.x, lane, at_seq);
+  if (warp == 8) w0 = find_work(sh, cu, blockIdx.x / PARTS, lane, at_seq);
   if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
   fence_before();
   __syncthreads();
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       while (ok) {
         const Work w = index < 0 ? Work{0, 0, 0, 0} : first ? w0 : find_work(sh, cu, index, lane, at_seq);
         first = false;
-        if (index >= 0) {
+        if (!SPLIT && index >= 0) {
           if (lane == 0) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the last answer has been read
             mbar_expect(stolen, 16);
@@ -351,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         if (index < 0 || !ok) break;
         if (w.len && lane == 0) {
-          const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
-          const int kvh = w.head(sh, 0) / sh.group;
+          const int nb0 = w.blocks<PARTS>(sh, 0, part), nb1 = w.blocks<PARTS>(sh, 1, part), nb = max(nb0, nb1);
+          const int kvh = w.head(sh, 0) / sh.group, key0 = w.first + w.first_block<PARTS>(sh, part) * kT;
           for (int x = 0; x < 2 * nb && ok; ++x, ++g) {             // K0 V0 K1 V1 ...
             const uint32_t s = g % kStages;
             if (g >= kStages) {
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             group_of[s] = groups + (x + 1) / 2;                      // K0 | V0 K1 | V1 K2 | ... | the last V
             mbar_expect(full0 + 8 * s, kTile);
             for (int c = 0; c < D / 64; ++c)
-              tma_3d(ring + s * kTile + c * kBox, (x & 1) ? &vmap : &kmap, full0 + 8 * s, 64 * c, kvh, w.first + (x >> 1) * kT);
+              tma_3d(ring + s * kTile + c * kBox, (x & 1) ? &vmap : &kmap, full0 + 8 * s, 64 * c, kvh, key0 + (x >> 1) * kT);
             if (x == 0) {
               for (int h = 0; h < 2 && ok; ++h) {
                 if (!(h ? nb1 : nb0)) continue;
@@ -383,6 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           groups += nb + 1;
         }
         __syncwarp();
+        if (SPLIT) {                             // one unit per cluster
+          ok = __all_sync(0xffffffffu, ok);
+          index = -1;
+          continue;
+        }
         const uint32_t parity = answers.next();
         bool got = mbar_wait(stolen, parity, wait_cycles);
         if (!got) mbar_wait(stolen, parity, kDrainCycles);
@@ -443,8 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             const Work w = work[u & 1];
             mbar_arrive(wempty + 8 * (u & 1));
             if (!w.len) return true;
-            const int nb0 = w.blocks(sh, 0), nb1 = w.blocks(sh, 1), nb = max(nb0, nb1);
-            const int tail = w.len % kT ? w.len / kT : nb; // the block inside which the sequence ends
+            const int nb0 = w.blocks<PARTS>(sh, 0, part), nb1 = w.blocks<PARTS>(sh, 1, part), nb = max(nb0, nb1);
+            if (SPLIT && !nb) continue;
+            // the block inside which the sequence ends
+            const int tail = w.len % kT ? w.len / kT - w.first_block<PARTS>(sh, part) : nb;
             if (!loaded(at)) return false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -498,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                   mma_commit(ofull + 8 * h);
                   // the first tile goes on to the next unit, if that is here,
                   // while the second one is still at this unit's last block
-                  if (h == 0) {
+                  if (!SPLIT && h == 0) {
                     Slot first = k;                        // of the next unit
                     if (nb1 > nb0) {
                       first.step();
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                     if (mbar_test(wfull + 8 * v, ((u + 1) >> 1) & 1) && work[v].len && is_loaded(first) &&
                         mbar_test(qfull, parities & kQ)) {
                       parities ^= kQ;
-                      score(0, first, work[v].blocks(sh, 0) == 1);
+                      score(0, first, work[v].blocks<PARTS>(sh, 0, part) == 1);
                       ahead = true;
                     }
                   }
@@ -536,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         __syncwarp();
         if (lane == 0) mbar_arrive(wempty + 8 * (u & 1));
         if (!w.len) break;
-        const int nb = max(w.blocks(sh, 0), w.blocks(sh, 1)), keys = w.len % kT;
-        if (keys && nb - 1 == w.len / kT) {
+        const int nb = max(w.blocks<PARTS>(sh, 0, part), w.blocks<PARTS>(sh, 1, part)), keys = w.len % kT;
+        if (keys && nb && w.first_block<PARTS>(sh, part) + nb - 1 == w.len / kT) {
           const uint32_t s = (g + 2 * nb - 1) % kStages;
           if (__any_sync(0xffffffffu, !mbar_wait(vask, asked.next(), wait_cycles))) break;
           for (int c = 0; c < D / 64; ++c)
@@ -555,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       for (int b = lane; b < sh.n_seq; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
       if (__any_sync(0xffffffffu, bad) && lane == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
     }
+    if (SPLIT) cluster_sync();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int h = warp >> 2, q = warp & 3;
@@ -564,6 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const uint64_t c2 = pair_of(sh.c, sh.c);
     Phase sn, on;
     bool ok = true;
+    Work shared_unit{0, 0, 0, 0};                          // SPLIT: the unit, and the row's maximum and sum here
+    float shared_m = 0.f, shared_l = 0.f;
     // an error recorded by an earlier call: everything runs, nothing is
     // written (the look at *info is under the first products)
     const bool write = !info_set(info);
@@ -578,13 +606,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(wempty + 8 * (u & 1));
       if (!w.len) break;
-      const int mine = w.blocks(sh, h);
+      const int mine = w.blocks<PARTS>(sh, h, part);
+      if (SPLIT) shared_unit = w;
       if (!mine) continue;
+      const int last = SPLIT ? w.row(sh, h) / kT - w.first_block<PARTS>(sh, part) : mine - 1;
       float m = -INFINITY;
       uint64_t l2[2] = {0, 0};                             // the row's sum, in four parts
       for (int j = 0; j < mine; ++j) {
         if (!wait(sfull + 8 * h, sn.next())) break;
-        const bool diagonal = j == mine - 1;
+        const bool diagonal = j == last;
         uint32_t s[4][32];
         tmem_ld32(ts, s[0]);
         tmem_ld32(ts + 32, s[1]);
@@ -642,7 +672,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       }
       if (!ok || !wait(ofull + 8 * h, on.next())) break;
       const float2 la = pair_to(l2[0]), lb = pair_to(l2[1]);
-      const float inv = 1.f / ((la.x + la.y) + (lb.x + lb.y));
+      const float l = (la.x + la.y) + (lb.x + lb.y);
+      if (SPLIT) {
+        shared_m = m;
+        shared_l = l;
+        continue;
+      }
+      const float inv = 1.f / l;
       const int row = w.row(sh, h) + r;
       uint64_t bad = 0;                                    // a sum of o * 0: NaN if one is not finite
       const uint64_t inv2 = pair_of(inv, inv);
@@ -686,10 +722,90 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       if (!(pair_to(bad).x + pair_to(bad).y == 0.f) && row < w.len) set_info(info, SGPT_INFO_NONFINITE);
     }
     if (!ok) failed = 1;
+    if constexpr (SPLIT) {
+      // Both tiles' products are done: their operands' place takes this
+      // part's O (fp32, rows of D with their 16-byte pieces swapped about so
+      // that neither side meets bank conflicts) and, behind it, m and l.
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const Work w = shared_unit;
+      const uint32_t ml = s0 + 2 * kT * D * 4;             // [2][kT] pairs
+      if (ok && w.blocks<PARTS>(sh, h, part)) {
+        const uint32_t line = s0 + (h * kT + r) * D * 4;
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t o[16];
+          tmem_ld16(to + 16 * i, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int piece = (4 * i + e) ^ (lane & 7);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + 16 * piece), "r"(o[4 * e]),
+                         "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
+                         : "memory");
+          }
+        }
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml + 8 * (h * kT + r)), "f"(shared_m), "f"(shared_l)
+                     : "memory");
+      }
+      cluster_sync();
+      bool all = write && w.len;
+      for (int p = 0; p < PARTS; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
+      // A warp takes whole rows, four columns a lane, with 16 loads of O in
+      // flight: one row at a time took 4 (width 64) to 8 us more in two parts.
+      constexpr int kAtOnce = 128 / D, kRows = 16 / PARTS;
+      const int piece = lane % (D / 4);
+#pragma unroll 1
+      for (int x0 = (part * 8 + warp) * kAtOnce + lane / (D / 4); x0 < 2 * kT && all; x0 += 16 * 8 * kAtOnce) {
+        int4 o[kRows][PARTS];
+        float pm[kRows][PARTS], pl[kRows][PARTS];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int x = x0 + 8 * PARTS * kAtOnce * i, g = x / kT;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            if (w.blocks<PARTS>(sh, g, p)) {
+              ld_cluster2(map_rank(ml + 8 * x, p), pm[i][p], pl[i][p]);
+              o[i][p] = ld_cluster4(map_rank(s0 + x * D * 4 + 16 * (piece ^ (x & 7)), p));
+            } else {
+              pm[i][p] = -INFINITY;
+              pl[i][p] = 0.f;
+              o[i][p] = make_int4(0, 0, 0, 0);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int x = x0 + 8 * PARTS * kAtOnce * i, g = x / kT, row = w.row(sh, g) + x % kT;
+          float top = pm[i][0], l = 0.f, y[4] = {}, bad = 0.f;
+#pragma unroll
+          for (int p = 1; p < PARTS; ++p) top = fmaxf(top, pm[i][p]);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const float f = ex2((pm[i][p] - top) * sh.c);
+            l = fmaf(f, pl[i][p], l);
+            y[0] = fmaf(f, __int_as_float(o[i][p].x), y[0]);
+            y[1] = fmaf(f, __int_as_float(o[i][p].y), y[1]);
+            y[2] = fmaf(f, __int_as_float(o[i][p].z), y[2]);
+            y[3] = fmaf(f, __int_as_float(o[i][p].w), y[3]);
+          }
+          if (row >= w.len) continue;
+          const float inv = 1.f / l;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] *= inv;
+            bad = fmaf(y[e], 0.f, bad);
+          }
+          *reinterpret_cast<uint2*>(O + (long long)(w.first + row) * sh.ldo + w.head(sh, g) * D + 4 * piece) =
+              make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+          if (!(bad == 0.f)) set_info(info, SGPT_INFO_NONFINITE);
+        }
+      }
+    }
   }
   fence_before();
   __syncthreads();
   if (failed && threadIdx.x == 0) set_info(info, SGPT_INFO_TIMEOUT);
+  if (SPLIT) cluster_sync();                               // no CTA leaves while its part is read
   if (warp == 9) tmem_free(tmem, kTmemCols);
 }
 
@@ -707,16 +823,66 @@ bool map_heads(CUtensorMap* m, const uint16_t* p, long long rows, int heads, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int PARTS>
 cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const int32_t* cu,
-                   const Shape& sh, long long ctas, uint16_t* O, int* info, cudaStream_t st) {
+                   const Shape& sh, long long units, uint16_t* O, int* info, cudaStream_t st) {
   static PerDevice attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_for(D));
+    return cudaFuncSetAttribute(attention_kernel<D, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_for(D));
   });
   if (e != cudaSuccess) return e;
-  return launch_after(attention_kernel<D>, (unsigned)ctas, kThreads, smem_for(D), 1, st, qm, km, vm, cu, sh, O, info,
-                      wait_limit_cycles());
+  return launch_after(attention_kernel<D, PARTS>, (unsigned)(units * PARTS), kThreads, smem_for(D), PARTS, st, qm, km,
+                      vm, cu, sh, O, info, wait_limit_cycles());
+}
+
+template <int D>
+cudaError_t launch_parts(int parts, const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                         const int32_t* cu, const Shape& sh, long long units, uint16_t* O, int* info, cudaStream_t st) {
+  return parts == 8   ? launch<D, 8>(qm, km, vm, cu, sh, units, O, info, st)
+         : parts == 4 ? launch<D, 4>(qm, km, vm, cu, sh, units, O, info, st)
+         : parts == 2 ? launch<D, 2>(qm, km, vm, cu, sh, units, O, info, st)
+                      : launch<D, 1>(qm, km, vm, cu, sh, units, O, info, st);
+}
+
+// Into how many parts the keys of a unit are split: the least of the times
+// (us) that this expects for sequences of one length (the longest of several
+// taken as half as long again: it decides, and only the device knows it). A
+// unit takes `block` for each block of its two tiles' keys and `start` once;
+// the launch takes its longest part, or all parts over the SMs. Fitted to
+// 134 launches of 1 to 32 heads on 1 to 12, 64 to 8192 rows; over these the
+// choice was 1.4 % off the best part count, and 1 part 25 %. One head of 8192
+// rows: 105 us in 1 part, 59 in 2, 35 in 4 (width 64); 8 heads on 2 of 3000
+// rows: 45 in 1, 28 in 2; 512 rows 12.0 in 1, 10.1 in 4. Clusters of four or eight CTAs find room for 32 and 14 at once (16
+// of eight took two waves): more are not tried, nor more parts than SMs where
+// several sequences leave each wave as long as the one before.
+int parts_for(long long n_tok, int n_seq, int head_units, bool pair, int D) {
+  constexpr float kStart[2][4] = {{5.8f, 8.3f, 8.3f, 9.2f}, {6.3f, 10.9f, 10.9f, 11.7f}};    // width; 1, 2, 4, 8 parts
+  const float block = D == 64 ? 1.6f : 1.7f;
+  const float* start = kStart[D == 128];
+  const float seqs = (float)std::min<long long>(n_seq, n_tok);
+  const int rows = pair ? kT : 2 * kT;
+  const int of_seq = (int)cdivll(cdivll(n_tok, n_seq), rows);                // units of rows
+  const float units = seqs * of_seq * head_units;
+  const float blocks = units * 0.5f * (pair ? of_seq + 1 : 2 * (of_seq + 1));    // of all units
+  int longest = (int)cdivll(n_seq > 1 ? cdivll(3 * n_tok, 2ll * n_seq) : n_tok, kT);
+  if (!pair && longest > 1) longest -= longest & 1;                          // one tile alone takes less than two
+  if (longest < 4) return 1;                                                 // at 3 blocks nothing gains 3 %
+  int best = 1;
+  float least = start[0] + std::max(block * longest, (block * blocks + 2 * (units - kNumSMs)) / kNumSMs);
+  for (int i = 1; i < 4; ++i) {
+    const int parts = 1 << i;
+    if ((i == 2 && units > 32) || (i == 3 && units > 14)) continue;
+    const bool waves = units * parts > kNumSMs;
+    if (waves && n_seq > 1) continue;
+    float t = std::max(start[i] + block * cdiv(longest, parts), (block * blocks + units * parts * start[i]) / kNumSMs);
+    if (waves) t *= 1.1f;
+    if (t < least) {
+      least = t;
+      best = parts;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -725,7 +891,8 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
 // all can have, for each unit of heads.
 long long attention_ctas(long long n_tok, int n_seq, int heads, int kv_heads) {
   const bool pair = heads / kv_heads % 2 == 0;
-  const long long units = n_tok / (pair ? kT : 2 * kT) + std::min<long long>(n_seq, n_tok);
+  const int unit_rows = pair ? kT : 2 * kT;      // a sequence's last unit may have one row only
+  const long long units = (n_tok + std::min<long long>(n_seq, n_tok) * (unit_rows - 1)) / unit_rows;
   return units * (pair ? heads / 2 : heads);
 }
 
@@ -745,9 +912,10 @@ cudaError_t launch_attention(const uint16_t* Q, long long ldq, const uint16_t* K
   sh.pair = sh.group % 2 == 0;
   sh.wide = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 && ldo % 16 == 0;
   sh.c = (float)((double)scale * 1.4426950408889634);
-  const long long ctas = attention_ctas(n_tok, n_seq, heads, kv_heads);
-  return D == 128 ? launch<128>(qm, km, vm, cu, sh, ctas, O, info, st)
-                  : launch<64>(qm, km, vm, cu, sh, ctas, O, info, st);
+  const long long units = attention_ctas(n_tok, n_seq, heads, kv_heads);
+  const int parts = parts_for(n_tok, n_seq, sh.pair ? heads / 2 : heads, sh.pair, D);
+  return D == 128 ? launch_parts<128>(parts, qm, km, vm, cu, sh, units, O, info, st)
+                  : launch_parts<64>(parts, qm, km, vm, cu, sh, units, O, info, st);
 }
 
 }  // namespace sgpt

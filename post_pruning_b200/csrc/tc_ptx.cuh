@@ -230,6 +230,9 @@ __device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void ld_cluster2(uint32_t addr, float& x, float& y) {
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void add_cluster(uint32_t addr, int32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
