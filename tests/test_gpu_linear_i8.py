@@ -269,6 +269,13 @@ def test_linear_i8_every_variant(n, d_in, d_out):
         assert bool((buf[n:] == -3).all())
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(384, 1024, 3101), (300, 2048, 4001), (384, 8224, 1542), (383, 8224, 1541)])
+def test_linear_i8_pairs_on_128_tokens(n, d_in, d_out):
+    """Pairs on tiles of 128 tokens, K in one part and in two, and their timeouts."""
+    test_linear_i8_every_variant(n, d_in, d_out)
+    test_linear_i8_wait_times_out(n, d_in, d_out)
+
+
 @pytest.mark.parametrize("n", [1, 24, 200])
 def test_linear_i8_many_tiles_per_cta(n):
     q, s, t, codes, grid, whole = _problem(n, 256, 60000)
