@@ -97,6 +97,25 @@ def test_attention_many_sequences():
     _check(_run(Q, K, V, off), Q, K, V, off)
 
 
+@pytest.mark.parametrize("heads,kv", [(2, 1), (1, 1)])
+def test_attention_many_sequences_of_several_units(heads, kv):
+    """Units are taken by length out of 32 sequences after 32; one with bad
+    offsets among them is reported and its neighbours are as they were."""
+    lens = [0, 700, 1, 128, 513, 0, 129, 300] * 9
+    Q, K, V, off = _inputs(lens, heads, kv, 64)
+    want = _run(Q, K, V, off)
+    _check(want, Q, K, V, off)
+    at = int(off[34])                                                     # inside the second 32
+    off[34] = -1
+    O = torch.full(Q.shape, 7.0, device=DEV).bfloat16()
+    info = pp.new_info()
+    pp.attention(Q, K, V, off, O, info)
+    assert pp.sync_status(info) == 1                                      # BAD_LENGTHS
+    lost = slice(int(off[33]), int(off[35]))                              # both sequences of that offset
+    assert at >= lost.start and bool((O[lost] == 7).all())
+    assert torch.equal(O[:lost.start], want[:lost.start]) and torch.equal(O[lost.stop:], want[lost.stop:])
+
+
 @pytest.mark.parametrize("heads,kv", [(4, 2), (3, 3)])
 def test_attention_strided_rows_and_rows_outside(heads, kv):
     """Q, K and V parts of one buffer, O a part of a wider one; rows before the
