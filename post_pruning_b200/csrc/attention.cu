@@ -857,36 +857,38 @@ cudaError_t launch_parts(int parts, const CUtensorMap& qm, const CUtensorMap& km
 
 // Into how many parts the keys of a unit are split: the least of the times
 // (us) that this expects for sequences of one length (the longest of several
-// taken as half as long again: it decides, and only the device knows it). A
-// unit takes `block` for each block of its two tiles' keys and `start` once;
-// the launch takes its longest part, or all parts over the SMs. Fitted to
-// 134 launches of 1 to 32 heads on 1 to 12, 64 to 8192 rows; over these the
-// choice was 1.4 % off the best part count, and 1 part 25 %. One head of 8192
-// rows: 105 us in 1 part, 59 in 2, 35 in 4 (width 64); 8 heads on 2 of 3000
-// rows: 45 in 1, 28 in 2; 512 rows 12.0 in 1, 10.1 in 4. Clusters of four or eight CTAs find room for 32 and 14 at once (16
-// of eight took two waves): more are not tried, nor more parts than SMs where
-// several sequences leave each wave as long as the one before.
+// taken as a quarter longer: it decides, and only the device knows it). A unit
+// takes `block` for each block of its two tiles' keys and `start` once; the
+// launch takes its longest part, or all parts over the SMs. Clusters of four
+// or eight CTAs find room for 32 and 14 at once (16 of eight took two waves),
+// and each further wave of them waits for the one before. Fitted to 336
+// launches of 1 to 32 heads on 1 to 32, 64 to 8192 rows; over these the choice
+// was 1.3 % off the best part count, and 1 part 23 %. One head of 8192 rows:
+// 105 us in 1 part, 59 in 2, 35 in 4 (width 64); 8 heads on 2 of 3000 rows: 45
+// in 1, 28 in 2; 512 rows 12.0 in 1, 10.1 in 4.
 int parts_for(long long n_tok, int n_seq, int head_units, bool pair, int D) {
   constexpr float kStart[2][4] = {{5.8f, 8.3f, 8.3f, 9.2f}, {6.3f, 10.9f, 10.9f, 11.7f}};    // width; 1, 2, 4, 8 parts
+  constexpr int kRoom[4] = {kNumSMs, kNumSMs / 2, 32, 14};
   const float block = D == 64 ? 1.6f : 1.7f;
   const float* start = kStart[D == 128];
-  const float seqs = (float)std::min<long long>(n_seq, n_tok);
+  const long long seqs = std::min<long long>(n_seq, n_tok);
   const int rows = pair ? kT : 2 * kT;
   const int of_seq = (int)cdivll(cdivll(n_tok, n_seq), rows);                // units of rows
-  const float units = seqs * of_seq * head_units;
+  const float units = (float)seqs * of_seq * head_units;
   const float blocks = units * 0.5f * (pair ? of_seq + 1 : 2 * (of_seq + 1));    // of all units
-  int longest = (int)cdivll(n_seq > 1 ? cdivll(3 * n_tok, 2ll * n_seq) : n_tok, kT);
+  int longest = (int)cdivll(n_seq > 1 ? cdivll(5 * n_tok, 4ll * n_seq) : n_tok, kT);
   if (!pair && longest > 1) longest -= longest & 1;                          // one tile alone takes less than two
   if (longest < 4) return 1;                                                 // at 3 blocks nothing gains 3 %
   int best = 1;
   float least = start[0] + std::max(block * longest, (block * blocks + 2 * (units - kNumSMs)) / kNumSMs);
   for (int i = 1; i < 4; ++i) {
     const int parts = 1 << i;
-    if ((i == 2 && units > 32) || (i == 3 && units > 14)) continue;
-    const bool waves = units * parts > kNumSMs;
-    if (waves && n_seq > 1) continue;
-    float t = std::max(start[i] + block * cdiv(longest, parts), (block * blocks + units * parts * start[i]) / kNumSMs);
-    if (waves) t *= 1.1f;
+    const float part = block * cdiv(longest, parts), all = (block * blocks + units * parts * start[i]) / kNumSMs;
+    float t = std::max(start[i] + part, all);
+    if (units > kRoom[i]) {
+      t = std::max(t, 1.1f * all);
+      if (i > 1) t = std::max(t, std::ceil(units / kRoom[i]) * start[i] + part);
+    }
     if (t < least) {
       least = t;
       best = parts;
