@@ -18,10 +18,14 @@
 // they take one product with the rounded 127/a.
 //   Bound by memory: 2 (gated: 4) bytes read and 1 written per element. A row
 // is read once: its threads hold it in registers between the maximum and the
-// codes. A warp takes a row up to 1024 elements, a CTA of 128 to 512 threads a
-// longer one, small enough that several rows are in flight per SM. A few long
-// rows (above 8192, n <= 64: decoding) are split over clusters of eight CTAs, which
-// exchange their maxima and sums.
+// codes. A warp takes a row up to 1024 elements, a CTA of 128 to 1024 threads a
+// longer one, small enough that several rows are in flight per SM, with no
+// more registers than the row needs (16384 gated rows of 5120 with four
+// vectors of eight per thread: 90 us; with the three that they need: 72). Of
+// 4096 rows on a warp takes up to 2048 elements too (gated: 1280): it has no
+// barrier to wait at (8192 rows of 1248 in a CTA each 10.2 us, in a warp 6.9;
+// 2048 rows 3.4 and 3.8). A few long rows (above 8192, n <= 64: decoding) are
+// split over clusters of eight CTAs, which exchange their maxima and sums.
 //
 // quant_codes_kernel: the integer codes of weights on their rows' grid
 // (scale, zero point), less half the levels so that they fit a signed byte.
@@ -237,17 +241,18 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
   if (t == 0 && part == 0) finish_row(rs, sum, scale + row, sums + row, info);
 }
 
-// The gated rows above 16384 elements, when there are many. A row takes 4
+// The gated rows of 20481 to 28672 elements, when there are many. A row takes 4
 // bytes per element in and more arithmetic than a CTA can hide behind its own
 // loads: persistent CTAs of 512 keep two rows of G and U in shared memory, one
-// copied in (bulk copies) while the other is quantized (4099 x 25600: 98 us,
-// 5.4 TB/s; with a row per CTA 161 us). Shorter rows are quicker with several
-// CTAs an SM (4096 x 11008: 59 us and 97).
-constexpr int kGatedThreads = 512, kGatedVec = 7;
+// copied in (bulk copies) while the other is quantized (8192 x 25600: 181 us,
+// 5.8 TB/s; with a row per CTA 273 us). Shorter rows are quicker with several
+// CTAs an SM (8192 x 20480: 132 us and 146), longer ones find no room for two.
+constexpr int kGatedThreads = 512, kGatedVec = 7;                    // vectors of a thread at most
 constexpr int kGatedMax = 28672;                                     // elements: two rows fill the shared memory
-static_assert(kGatedMax <= kGatedThreads * kGatedVec * 8, "a row in registers");
+static_assert(kGatedMax == kGatedThreads * kGatedVec * 8, "a row in registers");
 static_assert(2 * 4 * kGatedMax + 256 <= 232448, "dynamic shared memory per CTA");
 
+template <int VPT>
 __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
     const uint16_t* __restrict__ G, const uint16_t* __restrict__ Uu, long long n, int d, long long ldg, long long ldu,
     int8_t* __restrict__ Xq, float* __restrict__ scale, int32_t* __restrict__ sums, int* info, long long wait_cycles) {
@@ -291,10 +296,10 @@ __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
     if (failed) break;
     const uint4* g4 = reinterpret_cast<const uint4*>(rows_smem + 2 * b * row_bytes);
     const uint4* u4 = reinterpret_cast<const uint4*>(rows_smem + (2 * b + 1) * row_bytes);
-    float z[kGatedVec * 8];
+    float z[VPT * 8];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kGatedVec; ++i) {
+    for (int i = 0; i < VPT; ++i) {
       uint4 graw = make_uint4(0, 0, 0, 0), uraw = graw;
       if (t + i * kGatedThreads < vecs) {
         graw = g4[t + i * kGatedThreads];
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
     int sum = 0;
     uint2* q2 = reinterpret_cast<uint2*>(Xq + row * d);
 #pragma unroll
-    for (int i = 0; i < kGatedVec; ++i) {
+    for (int i = 0; i < VPT; ++i) {
       if (t + i * kGatedThreads >= vecs) continue;
       q2[t + i * kGatedThreads] = gated_codes(z + 8 * i, rs, sum);
     }
@@ -372,31 +377,50 @@ cudaError_t launch_as(const uint16_t* X, const uint16_t* U, long long n, int d, 
                       NT == 32 ? 256 : NT, 0, CL, st, X, U, n, d, ldx, ldu, Xq, scale, sums, info);
 }
 
+template <int VPT>
 cudaError_t launch_gated(const uint16_t* G, const uint16_t* U, long long n, int d, long long ldg, long long ldu,
                          int8_t* Xq, float* scale, int32_t* sums, int* info, cudaStream_t st) {
   static PerDevice attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(quant_gated_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * kGatedMax);
+    return cudaFuncSetAttribute(quant_gated_kernel<VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 4 * kGatedMax);
   });
   if (e != cudaSuccess) return e;
-  return launch_after(quant_gated_kernel, (unsigned)std::min<long long>(n, kNumSMs), kGatedThreads, 2 * 4 * (size_t)d, 1,
-                      st, G, U, n, d, ldg, ldu, Xq, scale, sums, info, wait_limit_cycles());
+  return launch_after(quant_gated_kernel<VPT>, (unsigned)std::min<long long>(n, kNumSMs), kGatedThreads,
+                      2 * 4 * (size_t)d, 1, st, G, U, n, d, ldg, ldu, Xq, scale, sums, info, wait_limit_cycles());
+}
+
+using LaunchFn = cudaError_t (*)(const uint16_t*, const uint16_t*, long long, int, long long, long long, int8_t*, float*,
+                                 int32_t*, int*, cudaStream_t);
+// The fewest vectors per thread, from VPT on, that hold the row.
+template <int NT, int VPT, int MOST, bool GATED>
+LaunchFn fit(int vecs) {
+  if constexpr (VPT < MOST)
+    if (vecs > NT * VPT) return fit<NT, VPT + 1, MOST, GATED>(vecs);
+  return launch_as<NT, VPT, 1, GATED>;
 }
 
 constexpr int kFewRows = 64;   // rows that do not fill the SMs with a CTA each
+constexpr int kManyRows = 4096;              // rows that suit a warp each up to kWarpVecs vectors per lane
+template <bool GATED>
+constexpr int kWarpVecs = GATED ? 5 : 8;
 
 template <bool GATED>
 cudaError_t launch(const uint16_t* X, const uint16_t* U, long long n, int d, long long ldx, long long ldu, int8_t* Xq,
                    float* scale, int32_t* sums, int* info, cudaStream_t st) {
   const auto as = [&](auto f) { return f(X, U, n, d, ldx, ldu, Xq, scale, sums, info, st); };
-  if (d <= 1024) return as(launch_as<32, 4, 1, GATED>);
-  if (d <= 4096) return as(launch_as<128, 4, 1, GATED>);
-  if (d <= 8192) return as(launch_as<256, 4, 1, GATED>);
+  const int vecs = d / 8;
+  if (vecs <= 32 * 4) return as(fit<32, 1, 4, GATED>(vecs));
+  if (n >= kManyRows && vecs <= 32 * kWarpVecs<GATED>) return as(fit<32, 5, kWarpVecs<GATED>, GATED>(vecs));
+  if (vecs <= 128 * 4) return as(fit<128, 2, 4, GATED>(vecs));
+  if (vecs <= 256 * 4) return as(fit<256, 3, 4, GATED>(vecs));
   if (n <= kFewRows) return as(launch_as<256, 2, 8, GATED>);
-  if constexpr (GATED)
-    if (d > 16384 && d <= kGatedMax) return launch_gated(X, U, n, d, ldx, ldu, Xq, scale, sums, info, st);
-  if (d <= 16384) return as(launch_as<256, 8, 1, GATED>);
-  if constexpr (GATED) return as(launch_as<512, 8, 1, GATED>);
+  if (vecs <= 256 * 8) return as(fit<256, 5, 8, GATED>(vecs));
+  if constexpr (GATED) {
+    if (vecs <= 512 * 5) return as(launch_as<512, 5, 1, true>);
+    if (vecs <= kGatedThreads * 6) return as(launch_gated<6>);
+    if (vecs <= kGatedThreads * kGatedVec) return as(launch_gated<kGatedVec>);
+    return as(launch_as<1024, 4, 1, true>);
+  }
   if (d <= 26624) return as(launch_as<256, 13, 1, false>);
   return as(launch_as<256, 16, 1, false>);
 }

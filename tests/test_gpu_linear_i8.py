@@ -62,6 +62,20 @@ def test_quant_tokens(n, d):
     _check_tokens(X, q, s, t)
 
 
+# every number of vectors per thread, a row per warp (many rows) and per CTA
+@pytest.mark.parametrize("n,d", [(21, 256), (21, 288), (20, 544), (19, 800), (130, 1056), (130, 2080), (66, 3104), (66, 6176),
+                                 (66, 8224), (66, 10272), (66, 12320), (66, 14368), (66, 16384)] +
+                         [(n, d) for n in (4095, 4096, 4101) for d in (1056, 1280, 1312, 1568, 1824, 2048, 2080)])
+def test_quant_tokens_vectors(n, d):
+    test_quant_tokens(n, d)
+    test_quant_tokens_silu(n, d, True)
+
+
+@pytest.mark.parametrize("n,d", [(65, 20480), (65, 20512), (300, 24576), (300, 24608), (65, 28672), (65, 28704)])
+def test_quant_tokens_silu_long_rows(n, d):
+    test_quant_tokens_silu(n, d, False)
+
+
 def test_quant_tokens_ties_and_extremes():
     """Every bf16 magnitude against largest values that make exact ties
     (254 x an odd multiple of the largest), and rows of huge, tiny and
