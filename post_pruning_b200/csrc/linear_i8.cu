@@ -17,9 +17,13 @@
 // stages by TMA (128-byte swizzle, out of range reads give zero codes), warp 1
 // issues four MMAs (K = 32) per stage, the others are the epilogue: four in the
 // split kernel, eight (two for the columns of each TMEM quarter) in the pair
-// kernel, where K is short and the epilogue not hidden: 256 -> 3080 with 3553
-// tokens in 16.0 us, 18.8 with four; 25600 wide either takes the same. Every
-// wait is bounded as everywhere in this library.
+// kernel, where K is short and the epilogue not hidden: 480 -> 15000 with 2000
+// tokens took 43 us with four and 36 with eight; 25600 wide either takes the
+// same. Every wait is bounded as everywhere in this library.
+//   What a tile's epilogue has beside its stores is kept short for the same
+// reason: its scales are fetched a tile ahead, its accumulator is handed back
+// without a release, tiles are decoded in 32 bits (those 36 us: 29; 608 ->
+// 23264 with 8192 tokens 215 us: 165). The stores are then what is left.
 //
 // linear_i8_pair_kernel, many tiles: persistent CTA pairs (cta_group::2) on
 // tiles of 256 channels x 256 (or 128) tokens, each CTA with half of the rows of both
@@ -92,15 +96,10 @@ struct Channel {             // one output channel's scale and shifted zero poin
   float scale;
   int zero;
 };
-__device__ __forceinline__ Channel channel(const Out& o, int row) {
-  Channel c{0.f, 0};
-  if (row < o.rows) {
-    const float2 g = *reinterpret_cast<const float2*>(o.grid + 2 * (long long)row);
-    c.scale = g.x;
-    c.zero = (int)g.y - o.half;
-  }
-  return c;
+__device__ __forceinline__ float2 grid_of(const Out& o, int row) {
+  return row < o.rows ? *reinterpret_cast<const float2*>(o.grid + 2 * (long long)row) : make_float2(0.f, 0.f);
 }
+__device__ __forceinline__ Channel channel(const Out& o, float2 g) { return Channel{g.x, (int)g.y - o.half}; }
 
 constexpr int kMaxSplit = 8;                    // parts of K at most
 
@@ -251,18 +250,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const _
   const int rows = out.rows, n = out.n;
   const int mt_count = cdiv(rows, 2 * kBM), nt_count = cdiv(n, BN), kt_count = cdiv(d, kBK);
   const int k0 = (int)((long long)kt_count * sp / split), k1 = (int)((long long)kt_count * (sp + 1) / split);
-  const long long items = (long long)mt_count * nt_count;
-  const int first_item = blockIdx.x / (2 * split), step = gridDim.x / (2 * split);
+  const uint32_t items = (uint32_t)mt_count * (uint32_t)nt_count;             // below 2^31, as the launch checks
+  const uint32_t first_item = blockIdx.x / (2 * split), step = gridDim.x / (2 * split);
   const uint32_t s0 = smem_u32(smem);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, mdone = tempty0 + 16;
-  auto decode = [&](long long w, int& mt, int& nt) {
-    const long long per_group = (long long)kGroupRows * nt_count;
-    const int g = (int)(w / per_group);
-    const int first = g * kGroupRows;
-    const int grows = min(kGroupRows, mt_count - first);
-    const long long r = w - g * per_group;
-    mt = first + (int)(r % grows);
+  auto decode = [&](uint32_t w, int& mt, int& nt) {
+    const uint32_t per_group = (uint32_t)kGroupRows * (uint32_t)nt_count;
+    const uint32_t first = w / per_group * kGroupRows, r = w % per_group;
+    const uint32_t grows = min((uint32_t)kGroupRows, (uint32_t)mt_count - first);
+    mt = (int)(first + r % grows);
     nt = (int)(r / grows);
   };
   if (threadIdx.x == 0) {
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const _
     if (elect_one()) {
       const uint32_t leader_full0 = map_rank(full0, leader);
       long long g = 0;
-      for (long long w = first_item; w < items && !failed; w += step) {
+      for (uint32_t w = first_item; w < items && !failed; w += step) {
         int mt, nt;
         decode(w, mt, nt);
         for (int i = k0; i < k1; ++i, ++g) {
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const _
       const uint64_t a_desc = sw128_desc(s0), b_desc = sw128_desc(s0 + kABytes);
       long long g = 0;
       int u = 0;
-      for (long long w = first_item; w < items && !failed; w += step, ++u) {
+      for (uint32_t w = first_item; w < items && !failed; w += step, ++u) {
         const int b = u & 1;
         if (u >= 2 && !mbar_wait(tempty0 + 8 * b, ((u >> 1) & 1) ^ 1, wait_cycles)) {
           failed = 1;
@@ -350,19 +347,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const _
     // TMEM lanes 32 q .. of this warp, and its half of the columns; epilogue thread
     const int q = warp & 3, part_of = (warp - 2) >> 2, et = threadIdx.x - 64;
     const uint32_t leader_tempty0 = map_rank(tempty0, leader);
+    // A tile's channel and token scales are asked for before the stores of the
+    // tile before it (asked for after them, they came 3300 cycles later) and
+    // touched after them.
+    float2 grid_next = make_float2(0.f, 0.f);
+    float scale_next = 0.f;
+    int sum_next = 0;
+    int mt_next = 0, nt_next = 0;
+    auto fetch = [&](uint32_t w) {
+      decode(w, mt_next, nt_next);
+      grid_next = grid_of(out, mt_next * 2 * kBM + (int)half * kBM + q * 32 + lane);
+      const int tok = nt_next * BN + et;
+      const bool in = et < BN && tok < n;
+      scale_next = in ? out.xs[tok] : 0.f;
+      sum_next = in ? out.xsum[tok] : 0;
+    };
+    if (first_item < items) fetch(first_item);
     int u = 0;
-    for (long long w = first_item; w < items; w += step, ++u) {
-      int mt, nt;
-      decode(w, mt, nt);
+    for (uint32_t w = first_item; w < items; w += step, ++u) {
+      const int mt = mt_next, nt = nt_next;
       const int b = u & 1, n0 = nt * BN, row = mt * 2 * kBM + (int)half * kBM + q * 32 + lane;
       const int cols = min(BN, n - n0);
-      for (int e = et; e < BN; e += 256) {
-        const bool in = e < cols;
-        tok_scale[b * BN + e] = in ? out.xs[n0 + e] : 0.f;
-        tok_sum[b * BN + e] = in ? out.xsum[n0 + e] : 0;
+      if (et < BN) {
+        tok_scale[b * BN + et] = scale_next;
+        tok_sum[b * BN + et] = sum_next;
       }
-      const Channel ch = channel(out, row);
+      const Channel ch = channel(out, grid_next);
       asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (w + step < items) fetch(w + step);
       int bad = failed;
       if (!bad) bad = !mbar_wait(tfull0 + 8 * b, (u >> 1) & 1, wait_cycles);
       bad = __any_sync(0xffffffffu, bad);      // one decision per warp: the TMEM loads are warp-collective
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_i8_pair_kernel(const _
     const int row0 = mt * 2 * kBM + (int)half * kBM;
     Channel ch4[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, row0 + 4 * lane + x);
+    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, grid_of(out, row0 + 4 * lane + x));
     cluster_sync();
     bool all = write;
     for (int p = 0; p < 2 * split; ++p) all = all && ld_cluster(map_rank(smem_u32(&failed), p)) == 0;
@@ -537,9 +549,9 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
       tok_scale[e] = out.xs[n0 + e];
       tok_sum[e] = out.xsum[n0 + e];
     }
-    ch = channel(out, row);
+    ch = channel(out, grid_of(out, row));
 #pragma unroll
-    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, mt * kBM + 4 * lane + x);
+    for (int x = 0; x < 4; ++x) ch4[x] = channel(out, grid_of(out, mt * kBM + 4 * lane + x));
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (__any_sync(0xffffffffu, !mbar_wait(tfull, 0, wait_cycles))) {
       failed = 1;
@@ -675,6 +687,7 @@ cudaError_t launch_pair(const Args& a, int split) {
   });
   if (e != cudaSuccess) return e;
   const long long items = (long long)cdiv(a.out.rows, 2 * kBM) * cdiv(a.out.n, BN);
+  if (items > INT32_MAX - kNumSMs) return cudaErrorInvalidValue;       // a Y of 2^47 values
   const int pairs = split > 1 ? (int)items * split : (int)std::min<long long>(items, kNumSMs / 2);
   return launch_after(linear_i8_pair_kernel<BN, T>, 2 * pairs, kPairThreads, pair_smem(BN), 2 * split, a.st, wm, xm, a.d,
                       split, a.out, a.info, wait_limit_cycles());

@@ -236,8 +236,11 @@ __device__ __forceinline__ void ld_cluster2(uint32_t addr, float& x, float& y) {
 __device__ __forceinline__ void add_cluster(uint32_t addr, int32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Arrives at a barrier of another CTA of the cluster, for TMEM that has been
+// read (tcgen05.wait::ld): nothing in memory is handed over, and a release
+// would wait for every store before it.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------- CTA pairs (cta_group::2)
