@@ -623,8 +623,8 @@ struct Args {
 };
 
 // Which kernel, how many tokens a tile, K in how many parts: the least of the
-// times (us) that these lines, fitted to every variant on nine layers (256 to
-// 25600 wide) with 1 to 2000 tokens, expect; over those the choice was 1.0 %
+// times (us) that these lines, fitted to every variant on eleven layers (256 to
+// 25600 wide) with 1 to 8000 tokens, expect; over those the choice was 1.1 %
 // off the best one. One token of 768 -> 768 took 4.3 us in clusters of three
 // and takes 2.9 in single CTAs, 333 tokens 5.8 in pairs and 3.1.
 //   The split kernel: a wave of 296 CTAs costs its start and epilogue, and
@@ -644,8 +644,8 @@ struct PlanLine {
   float start, wave, stage, split, part;
 };
 constexpr PlanLine kPlanLines[] = {{false, 16, 0.f, 2.6f, 0.13f, 1.0f, 0.46f},  {false, 32, 0.f, 2.8f, 0.147f, 0.7f, 0.6f},
-                                   {false, 64, 0.f, 3.3f, 0.19f, 0.76f, 0.51f}, {true, 128, 2.0f, 2.7f, 0.175f, 2.8f, 0.f},
-                                   {true, 256, 1.7f, 3.8f, 0.3f, 2.3f, 0.f}};
+                                   {false, 64, 0.f, 3.3f, 0.19f, 0.76f, 0.51f}, {true, 128, 3.1f, 1.5f, 0.173f, 3.0f, 0.f},
+                                   {true, 256, 2.7f, 2.7f, 0.295f, 2.5f, 0.f}};
 
 Plan plan(int rows, int n, int d) {
   const int kt = cdiv(d, kBK);
