@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(kThreads) linear_i8_split_kernel(const __grid_
   const int rank = (int)cluster_rank();                    // this CTA's part of K
   const int tile = blockIdx.x / split;
   const int rows = out.rows, n = out.n;
-  const int mt_count = cdiv(rows, kBM), kt_count = cdiv(d, kBK);
-  const int mt = tile % mt_count, nt = tile / mt_count;
+  const int nt_count = cdiv(n, BN), kt_count = cdiv(d, kBK);
+  const int mt = tile / nt_count, nt = tile % nt_count;      // token tiles fastest: they read the same codes together
   const int k0 = (int)((long long)kt_count * rank / split), k1 = (int)((long long)kt_count * (rank + 1) / split);
   const uint32_t s0 = smem_u32(smem);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, tfull = empty0 + 8 * kStages, mdone = tfull + 8;
@@ -623,8 +623,8 @@ struct Args {
 };
 
 // Which kernel, how many tokens a tile, K in how many parts: the least of the
-// times (us) that these lines, fitted to every variant on eleven layers (256 to
-// 25600 wide) with 1 to 8000 tokens, expect; over those the choice was 1.1 %
+// times (us) that these lines, fitted to every variant on 18 layers (256 to
+// 28672 wide) with 1 to 8000 tokens, expect; over those the choice was 1.7 %
 // off the best one. One token of 768 -> 768 took 4.3 us in clusters of three
 // and takes 2.9 in single CTAs, 333 tokens 5.8 in pairs and 3.1.
 //   The split kernel: a wave of 296 CTAs costs its start and epilogue, and
@@ -633,7 +633,10 @@ struct Args {
 // The pair kernel: waves of 74 pairs; K in more than two is not tried there:
 // clusters of eight such CTAs do not all find room at once (16 of them took
 // two waves); clusters of seven CTAs of the split kernel did not either.
-//   Codes that the L2 does not hold come at 6 TB/s, and at 60 GB/s a CTA.
+//   Codes that the L2 does not hold come at 6.2 TB/s, and at 70 GB/s a CTA;
+// another tile of tokens that reads them at about the same time costs 0.45 as
+// much again (17 tokens of 20608 -> 25568: 120 us in two tiles of 16 one after
+// the other, 93 side by side, 80 in one of 32).
 struct Plan {
   bool pair;
   int bn, split;
@@ -643,9 +646,9 @@ struct PlanLine {
   int bn;
   float start, wave, stage, split, part;
 };
-constexpr PlanLine kPlanLines[] = {{false, 16, 0.f, 2.6f, 0.13f, 1.0f, 0.46f},  {false, 32, 0.f, 2.8f, 0.147f, 0.7f, 0.6f},
-                                   {false, 64, 0.f, 3.3f, 0.19f, 0.76f, 0.51f}, {true, 128, 3.1f, 1.5f, 0.173f, 3.0f, 0.f},
-                                   {true, 256, 2.7f, 2.7f, 0.295f, 2.5f, 0.f}};
+constexpr PlanLine kPlanLines[] = {{false, 16, 0.f, 2.6f, 0.13f, 1.0f, 0.46f},   {false, 32, 0.f, 2.8f, 0.141f, 0.8f, 0.55f},
+                                   {false, 64, 0.f, 2.9f, 0.196f, 1.16f, 0.51f}, {true, 128, 3.1f, 1.7f, 0.161f, 2.8f, 0.f},
+                                   {true, 256, 2.7f, 2.9f, 0.289f, 2.3f, 0.f}};
 
 Plan plan(int rows, int n, int d) {
   const int kt = cdiv(d, kBK);
@@ -664,7 +667,9 @@ Plan plan(int rows, int n, int d) {
       if (split > 1) t += l.split + l.part * (split - 1);
       if (codes > 32e6f) {
         const float ctas = (float)std::min(units, room) * (l.pair ? 2 : 1);
-        t = std::max(t, 3.f + codes / std::min(6.0e6f, ctas * 6.0e4f));
+        // (of two that wait for the codes alike, the one with less else to do)
+        const float reads = 1.f + 0.45f * (cdiv(n, l.bn) - 1);
+        t = std::max(t, 3.2f + codes * reads / std::min(6.2e6f, ctas * 7.0e4f) + 0.001f * t);
       }
       if (t < least) {
         least = t;

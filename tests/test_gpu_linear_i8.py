@@ -290,6 +290,15 @@ def test_linear_i8_pairs_on_128_tokens(n, d_in, d_out):
     test_linear_i8_wait_times_out(n, d_in, d_out)
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(475, 5280, 523), (290, 9120, 387), (194, 29440, 290), (845, 1056, 1285),
+                                          (789, 5280, 645), (200, 25600, 5001), (17, 20608, 2050), (50, 14336, 1000)])
+def test_linear_i8_wide_tiles_with_k_split(n, d_in, d_out):
+    """Tiles of 64 tokens with K in two, four and eight, pairs on 128 and 256
+    tokens with K in one and two, a few tokens of long rows."""
+    test_linear_i8_every_variant(n, d_in, d_out)
+    test_linear_i8_wait_times_out(n, d_in, d_out)
+
+
 @pytest.mark.parametrize("n", [1, 24, 200])
 def test_linear_i8_many_tiles_per_cta(n):
     q, s, t, codes, grid, whole = _problem(n, 256, 60000)
