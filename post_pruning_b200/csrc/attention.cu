@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         first = false;
         if (!SPLIT && index >= 0) {
           if (lane == 0) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the last answer has been read
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // this lane has read the last answer
             mbar_expect(stolen, 16);
             steal_cta(smem_u32(answer), stolen);
           }
@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         if (!got) mbar_wait(stolen, parity, kDrainCycles);
         asked = false;
         ok = __all_sync(0xffffffffu, ok && got);
-        index = stolen_cta(smem_u32(answer));
+        // by lane 0 alone: no other lane's read has to be ordered before the next answer
+        index = __shfl_sync(0xffffffffu, lane == 0 ? stolen_cta(smem_u32(answer)) : 0, 0);
       }
       if (!ok && lane == 0) {
         failed = 1;
