@@ -408,7 +408,7 @@ sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* 
  *     sequence are not written. Offsets that decrease or leave [0, n_tok] set
  *     SGPT_INFO_BAD_LENGTHS (the output is then unspecified).
  *   width 64 or 128 (else SGPT_ERR_UNSUPPORTED), heads a multiple of
- *     kv_heads, scale > 0 (usually width^-1/2), 0 <= n_tok <= 2^30.
+ *     kv_heads, scale > 0 (usually width^-1/2), 0 <= n_tok, n_seq <= 2^30.
  * Scores, softmax and sums in fp32; the softmax's weights enter the second
  * product in bf16; O is rounded once. Values in masked places (later rows,
  * other sequences, rows outside) never reach a row's result as long as the

@@ -63,6 +63,9 @@ sgpt_status check_ws(void* ws, size_t have, size_t need) {
 // Tokens or packed rows of the 8-bit forward and the attention: row indices
 // plus a tile stay inside an int.
 bool valid_rows(int64_t n) { return n >= 0 && n <= (int64_t(1) << 30); }
+// Sequences, which kernels walk in strides of 32: their number plus a stride
+// stays inside an int.
+bool valid_seqs(int n_seq) { return n_seq >= 0 && n_seq <= (1 << 30); }
 // A bf16 row stride: rows start on 16-byte boundaries.
 bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0 && ld <= (int64_t(1) << 31); }
 
@@ -378,7 +381,7 @@ sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* 
 sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
                            int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
                            int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream) {
-  if (!valid_rows(n_tok) || n_seq < 0 || !dev_info || heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536)
+  if (!valid_rows(n_tok) || !valid_seqs(n_seq) || !dev_info || heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536)
     return SGPT_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || width < 1) return SGPT_ERR_INVALID_ARG;
   if (width != 64 && width != 128) return SGPT_ERR_UNSUPPORTED;
@@ -410,7 +413,7 @@ sgpt_status sgpt_prune_attn_block(const sgpt_attn_block* blk, int hidden, int he
                                   float scale, const uint16_t* X, int64_t n_tok, const int32_t* offsets, int n_seq,
                                   int mode, const sgpt_params* p, uint16_t* X_next, uint16_t* A, void* ws,
                                   size_t ws_bytes, int* dev_info, void* stream) {
-  if (!blk || !X || !X_next || !offsets || !dev_info || n_seq < 0) return SGPT_ERR_INVALID_ARG;
+  if (!blk || !X || !X_next || !offsets || !dev_info || !valid_seqs(n_seq)) return SGPT_ERR_INVALID_ARG;
   const void* ptrs[] = {blk->W_q, blk->W_k, blk->W_v, blk->W_o, blk->mask_q, blk->mask_k, blk->mask_v, blk->mask_o,
                         X, X_next};
   for (const void* q : ptrs)
