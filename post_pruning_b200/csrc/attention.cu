@@ -240,6 +240,13 @@ __device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lan
   return w;
 }
 
+// Every offset is looked at once, by one warp.
+__device__ void check_offsets(const Shape& sh, const int32_t* cu, int lane, int* info) {
+  bool bad = false;
+  for (int b = lane; b < sh.n_seq; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
+  if (__any_sync(0xffffffffu, bad) && lane == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
+}
+
 __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* v, bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -423,6 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         ok = __all_sync(0xffffffffu, ok && got);
         // by lane 0 alone: no other lane's read has to be ordered before the next answer
         index = __shfl_sync(0xffffffffu, lane == 0 ? stolen_cta(smem_u32(answer)) : 0, 0);
+        // the first CTA looks at the offsets; which CTAs are taken is not
+        // specified, so whoever takes that one does it instead
+        if (index == 0) check_offsets(sh, cu, lane, info);
       }
       if (!ok && lane == 0) {
         failed = 1;
@@ -586,10 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         g += 2 * nb;
       }
     } else if (blockIdx.x == 0) {
-      // every offset is looked at once
-      bool bad = false;
-      for (int b = lane; b < sh.n_seq; b += 32) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > sh.n_tok;
-      if (__any_sync(0xffffffffu, bad) && lane == 0) set_info(info, SGPT_INFO_BAD_LENGTHS);
+      check_offsets(sh, cu, lane, info);
     }
     if (SPLIT) cluster_sync();
   } else {

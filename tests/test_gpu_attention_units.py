@@ -29,3 +29,28 @@ def test_attention_more_ctas_than_units(heads, kv, width):
     _check(want, Q, K, V, off)
     for _ in range(20):
         assert torch.equal(_run(Q, K, V, packed), want)
+
+
+@pytest.mark.parametrize("heads,kv,width", [(16, 4, 128), (7, 7, 64)])
+def test_attention_bad_offsets_in_a_crowded_launch(heads, kv, width):
+    """Bad offsets are reported whichever CTAs of the launch start and whichever
+    are taken: the SMs are still full of another stream's launch."""
+    lens = [200, 129, 1, 300] * 12
+    Q, K, V, off = _inputs(lens, heads, kv, width)
+    other = _inputs([2000] * 4, 8, 8, 128, seed=1)
+    away = torch.empty_like(other[0])
+    streams, infos = [torch.cuda.Stream(), torch.cuda.Stream()], [pp.new_info(), pp.new_info()]
+    for i in (0, 20, len(lens) - 1):
+        bad = off.clone()
+        bad[i + 1] = off[-1] + 1 if i + 1 == len(lens) else off[i] - 1
+        torch.cuda.synchronize()
+        for _ in range(5):
+            pp.info_clear(infos[1], stream=streams[1])
+            with torch.cuda.stream(streams[0]):
+                pp.attention(*other, away, infos[0])
+            with torch.cuda.stream(streams[1]):
+                O = torch.empty_like(Q)
+                pp.attention(Q, K, V, bad, O, infos[1])
+            assert pp.sync_status(infos[1], streams[1]) == 1                  # BAD_LENGTHS
+    torch.cuda.synchronize()
+    assert pp.sync_status(infos[0]) == 0
