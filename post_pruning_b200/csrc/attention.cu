@@ -294,8 +294,7 @@ struct Phase {
 template <int D, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-    const __grid_constant__ CUtensorMap vmap, const int32_t* __restrict__ cu, const Shape sh,
-    uint16_t* __restrict__ O, int* info, const long long wait_cycles) {
+    const __grid_constant__ CUtensorMap vmap, const int32_t* cu, const Shape sh, uint16_t* O, int* info, const long long wait_cycles) {
   constexpr int kTile = tile_bytes(D), kStages = stages_for(D);
   constexpr bool SPLIT = PARTS > 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];

@@ -165,8 +165,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, uint32_t*
 // most VPT vectors of 8 elements per thread.
 template <int NT, int VPT, int CL, bool GATED>
 __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
-    const uint16_t* __restrict__ X, const uint16_t* __restrict__ Uu, long long n, int d, long long ldx, long long ldu,
-    int8_t* __restrict__ Xq, float* __restrict__ scale, int32_t* __restrict__ sums, int* info) {
+    const uint16_t* X, const uint16_t* Uu, long long n, int d, long long ldx, long long ldu, int8_t* __restrict__ Xq,
+    float* __restrict__ scale, int32_t* __restrict__ sums, int* info) {
   constexpr int kRows = NT == 32 ? 8 : 1;          // rows per CTA
   __shared__ uint32_t red[2][32], mine[2];
   const int part = CL > 1 ? (int)ptx::cluster_rank() : 0;
@@ -184,14 +184,14 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) quant_tokens_kernel(
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (v0 + i * step < vecs) raw[i] = __ldcs(x4 + v0 + i * step);
+    if (v0 + i * step < vecs) raw[i] = ptx::ld_once(x4 + v0 + i * step);
   }
   uint4 rawu[GATED ? VPT : 1];
   if constexpr (GATED) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       rawu[i] = make_uint4(0, 0, 0, 0);
-      if (v0 + i * step < vecs) rawu[i] = __ldcs(u4 + v0 + i * step);
+      if (v0 + i * step < vecs) rawu[i] = ptx::ld_once(u4 + v0 + i * step);
     }
   }
   const bool skip = cta_info_set(info);            // under the row's loads
@@ -254,8 +254,8 @@ static_assert(2 * 4 * kGatedMax + 256 <= 232448, "dynamic shared memory per CTA"
 
 template <int VPT>
 __global__ void __launch_bounds__(kGatedThreads, 1) quant_gated_kernel(
-    const uint16_t* __restrict__ G, const uint16_t* __restrict__ Uu, long long n, int d, long long ldg, long long ldu,
-    int8_t* __restrict__ Xq, float* __restrict__ scale, int32_t* __restrict__ sums, int* info, long long wait_cycles) {
+    const uint16_t* G, const uint16_t* Uu, long long n, int d, long long ldg, long long ldu, int8_t* __restrict__ Xq,
+    float* __restrict__ scale, int32_t* __restrict__ sums, int* info, long long wait_cycles) {
   extern __shared__ __align__(128) unsigned char rows_smem[];         // [2][G row, U row]
   __shared__ uint64_t full[2];
   __shared__ uint32_t red[2][32];

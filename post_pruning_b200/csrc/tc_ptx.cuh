@@ -174,6 +174,18 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What a predecessor may have written is read by ordinary loads after the
+// wait: such a pointer is no const __restrict__ parameter, whose loads would
+// count as invariant over the whole kernel. 16 bytes that are read once:
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------- grid as a queue
 //
 // Asks for the index of a CTA of this grid that has not started yet: the
