@@ -1,12 +1,13 @@
 """Build libsgpt.so (the C-ABI solver library) in-tree with nvcc for sm_100a,
 and the binding's argument marshalling (_marshal, host code) with the C++
-compiler.
+compiler. The library does without the latter: where it cannot be compiled,
+that is said and the build goes on.
 
     python -m post_pruning_b200.build [--verbose-ptxas]
 
 Objects go to post_pruning_b200/_build/, the library to
 post_pruning_b200/libsgpt.so, the extension module beside it. Only sources
-newer than their object are recompiled.
+newer than their object are recompiled; the extension module also when torch is another one.
 """
 
 from __future__ import annotations
@@ -62,21 +63,26 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
 
 def _build_marshal() -> None:
     """csrc/marshal.cpp against the installed torch's headers (host code only)."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgpt.h")))
-    if os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
-        return
     import torch
+    src, stamp = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.torch")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgpt.h")))
+    if os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == torch.__version__:
+                return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DSGPT_TORCH_VERSION="{torch.__version__}"',
            *("-I" + d for d in (os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
                                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
            src, "-o", MARSHAL, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
 
 
 def build(ptxas_verbose: bool = False) -> str:
@@ -85,7 +91,10 @@ def build(ptxas_verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
-        marshal.result()
+        try:
+            marshal.result()
+        except Exception as e:         # no C++ compiler, no torch headers: calls are marshalled in Python then
+            print(f"_marshal was not built, calls will take 5-9 us more of host time:\n{e}", file=sys.stderr)
     if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
         return LIB
     cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"]

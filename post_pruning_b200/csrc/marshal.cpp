@@ -3,7 +3,8 @@
 // The same checks as the Python functions of sgpt.py, which make up most of
 // such a call's host time there. Nothing is computed here, and no argument
 // error is reported: a call that is not plainly valid returns -1, and the
-// Python function repeats the checks, raises or makes the call itself.
+// Python function repeats the checks, raises or makes the call itself (as it
+// makes every call where this module is not there).
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDAFunctions.h>
@@ -180,4 +181,12 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module_def); }
+// With the torch it was compiled against: the binding takes it for that one only.
+PyMODINIT_FUNC PyInit__marshal(void) {
+  PyObject* m = PyModule_Create(&module_def);
+  if (m && PyModule_AddStringConstant(m, "torch_version", SGPT_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

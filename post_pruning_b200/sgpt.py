@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from dataclasses import dataclass, field
 
 import torch
@@ -162,11 +163,27 @@ def lib() -> ctypes.CDLL:
         f.restype = res
         f.argtypes = args
     global _marshal
-    from . import _marshal as m        # built with the library; missing: ImportError
-    m.bind(*(ctypes.cast(getattr(L, "sgpt_" + name), vp).value for name in
-             ("quant_tokens", "quant_tokens_silu", "linear_i8", "attention")))
-    _lib, _marshal = L, m
+    _lib, _marshal = L, _load_marshal(L)
     return L
+
+
+def _load_marshal(L):
+    """The extension module, built with the library; None where there is none
+    for this torch (the Python functions then make every call)."""
+    try:
+        from . import _marshal as m
+    except ImportError as e:
+        why = str(e)
+    else:
+        built = getattr(m, "torch_version", None)
+        if built == torch.__version__:
+            m.bind(*(ctypes.cast(getattr(L, "sgpt_" + name), ctypes.c_void_p).value for name in
+                     ("quant_tokens", "quant_tokens_silu", "linear_i8", "attention")))
+            return m
+        why = f"it was built for torch {built}"
+    warnings.warn("post_pruning_b200._marshal is not used, calls take 5-9 us more of host time "
+                  f"(python -m post_pruning_b200.build builds it): {why}", RuntimeWarning, stacklevel=3)
+    return None
 
 
 # ------------------------------------------------------------------ helpers

@@ -1,0 +1,58 @@
+"""The binding's two ways to a call that is made per token and layer: through
+the extension module and through the Python functions alone."""
+
+import pytest
+import torch
+
+import post_pruning_b200 as pp
+from post_pruning_b200 import sgpt as S
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _operands():
+    g = torch.Generator(device=DEV).manual_seed(2)
+    n, d, rows, heads, width = 37, 512, 96, 4, 64
+    wide = torch.randn(n, 2 * d, device=DEV, generator=g).bfloat16()
+    codes = torch.randint(-128, 128, (rows, d), device=DEV, generator=g).to(torch.int8)
+    grid = torch.stack([torch.rand(rows, device=DEV, generator=g) + 0.01, torch.full((rows,), 100.0, device=DEV)], 1).contiguous()
+    qkv = torch.randn(n, 3 * heads * width, device=DEV, generator=g).bfloat16()
+    off = torch.tensor([0, 11, 11, n], dtype=torch.int32, device=DEV)
+    return n, d, wide, codes, grid, qkv, heads, width, off
+
+
+def _pass(info):
+    """Every call once; all outputs."""
+    n, d, wide, codes, grid, qkv, heads, width, off = _operands()
+    out = []
+    for gated in (False, True):
+        q, s, t = (torch.empty(n, d, dtype=torch.int8, device=DEV), torch.empty(n, device=DEV),
+                   torch.empty(n, dtype=torch.int32, device=DEV))
+        if gated:
+            pp.quant_tokens_silu(wide[:, :d], wide[:, d:], q, s, t, info)
+        else:
+            pp.quant_tokens(wide[:, d:], q, s, t, info)
+        out += [q, s, t]
+        for dtype in (torch.float32, torch.bfloat16):
+            out.append(torch.empty(n, codes.shape[0], dtype=dtype, device=DEV))
+            pp.linear_i8(q, s, t, codes, grid, out[-1], info)
+    q, k, v = (x.unflatten(1, (heads, width)) for x in qkv.chunk(3, 1))
+    for scale in (None, 0.25):
+        out.append(torch.empty(n, heads, width, dtype=torch.bfloat16, device=DEV))
+        pp.attention(q, k, v, off, out[-1], info, scale=scale)
+    return out
+
+
+def test_python_functions_alone_give_the_same_bits(monkeypatch):
+    info = pp.new_info()
+    pp.lib()
+    assert S._marshal is not None
+    want = _pass(info)
+    monkeypatch.setattr(S, "_marshal", None)
+    before = pp.kernel_launches()
+    for got, ref in zip(_pass(info), want):
+        assert torch.equal(got, ref)
+    assert pp.kernel_launches() == before + 8
+    pp.raise_on_info(info)
