@@ -218,6 +218,14 @@ def _one_device(*tensors: torch.Tensor) -> int:
     return dev
 
 
+def _one_word(dev_info: torch.Tensor):
+    """dev_info: an int32 tensor whose first word the kernels read and write."""
+    if dev_info.dtype is not torch.int32:
+        raise TypeError("dev_info must be int32")
+    if dev_info.numel() < 1:
+        raise ValueError("dev_info must have one word")
+
+
 # the handle of a device's current stream, without the Stream object that
 # torch.cuda.current_stream() builds (3 us of a call that takes 6)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -481,7 +489,9 @@ def quant_codes(W: torch.Tensor, grid: torch.Tensor, codes: torch.Tensor, dev_in
     r, d = W.shape
     if grid.shape != (r, 2) or codes.shape != (r, d) or not grid.is_contiguous() or not codes.is_contiguous():
         raise ValueError("grid must be contiguous [d_out, 2] and codes contiguous [d_out, d_in]")
-    _enqueue("sgpt_quant_codes", _one_device(W, grid, codes, dev_info), stream, _ptr(W), r, d, ldw, _ptr(grid), qbits,
+    dev = _one_device(W, grid, codes, dev_info)
+    _one_word(dev_info)
+    _enqueue("sgpt_quant_codes", dev, stream, _ptr(W), r, d, ldw, _ptr(grid), qbits,
              _ptr(codes), _ptr(dev_info))
 
 
@@ -512,6 +522,7 @@ def quant_tokens(X: torch.Tensor, Xq: torch.Tensor, scale: torch.Tensor, sums: t
         if status > 0:
             raise SgptError(status, "sgpt_quant_tokens")
     dev = _one_device(X, Xq, scale, sums, dev_info)
+    _one_word(dev_info)
     if X.dtype is not torch.bfloat16:
         raise TypeError("X must be bfloat16")
     ldx = _row_stride(X, "X")
@@ -532,6 +543,7 @@ def quant_tokens_silu(G: torch.Tensor, U: torch.Tensor, Xq: torch.Tensor, scale:
         if status > 0:
             raise SgptError(status, "sgpt_quant_tokens_silu")
     dev = _one_device(G, U, Xq, scale, sums, dev_info)
+    _one_word(dev_info)
     if not (G.dtype is torch.bfloat16 and U.dtype is torch.bfloat16):
         raise TypeError("G and U must be bfloat16")
     ldg, ldu = _row_stride(G, "G"), _row_stride(U, "U")
@@ -555,6 +567,7 @@ def linear_i8(Xq: torch.Tensor, scale: torch.Tensor, sums: torch.Tensor, codes: 
         if status > 0:
             raise SgptError(status, "sgpt_linear_i8")
     dev = _one_device(Xq, scale, sums, codes, grid, Y, dev_info)
+    _one_word(dev_info)
     y_bf16 = Y.dtype is torch.bfloat16
     if not (codes.dtype is torch.int8 and grid.dtype is torch.float32 and (y_bf16 or Y.dtype is torch.float32)):
         raise TypeError("codes must be int8, grid float32 and Y float32 or bfloat16")
@@ -594,6 +607,7 @@ def attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, offsets: torch.
         if status > 0:
             raise SgptError(status, "sgpt_attention")
     dev = _one_device(Q, K, V, offsets, O, dev_info)
+    _one_word(dev_info)
     ldq, ldk, ldv, ldo = _heads_stride(Q, "Q"), _heads_stride(K, "K"), _heads_stride(V, "V"), _heads_stride(O, "O")
     n, heads, width = shape = Q.shape
     kv_heads = K.shape[1]
@@ -671,6 +685,7 @@ def prune_attn_block(W_q: torch.Tensor, W_k: torch.Tensor, W_v: torch.Tensor, W_
     if width < 1 or dq % width or dk % width:
         raise ValueError("the rows of W_q, W_k and W_v are whole heads of `width`")
     dev = _one_device(W_q, W_k, W_v, W_o, *masks, X, offsets, X_next, ws, dev_info, *(() if A is None else (A,)))
+    _one_word(dev_info)
     for t, name, shape in ((W_q, "W_q", (dq, hidden)), (W_k, "W_k", (dk, hidden)), (W_v, "W_v", (dk, hidden)),
                            (W_o, "W_o", (hidden, dq))):
         _dev(t, torch.float32, name)

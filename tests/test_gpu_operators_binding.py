@@ -56,3 +56,33 @@ def test_python_functions_alone_give_the_same_bits(monkeypatch):
         assert torch.equal(got, ref)
     assert pp.kernel_launches() == before + 8
     pp.raise_on_info(info)
+
+
+@pytest.mark.parametrize("alone", [False, True])
+@pytest.mark.parametrize("bad,error", [(dict(dtype=torch.int64), TypeError), (dict(dtype=torch.uint8), TypeError),
+                                       (dict(dtype=torch.float32), TypeError), (dict(size=0), ValueError)])
+def test_the_error_word_is_an_int32(bad, error, alone, monkeypatch):
+    """A kernel writes four bytes there: a shorter or emptier tensor is refused,
+    a longer type would not read as the code."""
+    info = torch.zeros(bad.get("size", 1), dtype=bad.get("dtype", torch.int32), device=DEV)
+    n, d, wide, codes, grid, qkv, heads, width, off = _operands()
+    q, s, t = (torch.empty(n, d, dtype=torch.int8, device=DEV), torch.empty(n, device=DEV),
+               torch.empty(n, dtype=torch.int32, device=DEV))
+    qh = qkv[:, :heads * width].unflatten(1, (heads, width))
+    W = [torch.zeros(256, 256, device=DEV) for _ in range(4)]
+    masks = [torch.zeros(256, 8, dtype=torch.int32, device=DEV) for _ in range(4)]
+    X = torch.zeros(n, 256, dtype=torch.bfloat16, device=DEV)
+    ws = pp.attn_block_workspace(256, 4, 4, 64, n)
+    pp.lib()
+    if alone:
+        monkeypatch.setattr(S, "_marshal", None)
+    before = pp.kernel_launches()
+    for call in (lambda: pp.quant_codes(torch.zeros(96, d, device=DEV), grid, codes, info),
+                 lambda: pp.quant_tokens(wide[:, d:], q, s, t, info),
+                 lambda: pp.quant_tokens_silu(wide[:, :d], wide[:, d:], q, s, t, info),
+                 lambda: pp.linear_i8(q, s, t, codes, grid, torch.empty(n, 96, device=DEV), info),
+                 lambda: pp.attention(qh, qh, qh, off, torch.empty_like(qh), info),
+                 lambda: pp.prune_attn_block(*W, masks, X, off, 64, pp.Params("2:4"), torch.empty_like(X), ws, info)):
+        with pytest.raises(error):
+            call()
+    assert pp.kernel_launches() == before
