@@ -438,8 +438,9 @@ sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, in
  * blk: the four weight matrices (fp32, row-major, in: dense, out: pruned;
  *   W_q [heads * width x hidden], W_k, W_v [kv_heads * width x hidden],
  *   W_o [hidden x heads * width]) and their masks ([rows x cols / 32]).
- * X, X_next [n_tok x hidden] bf16; A [n_tok x heads * width] bf16 out (o's
- *   input), or NULL to keep it in ws.
+ * X, X_next [n_tok x hidden] bf16, the same buffer or two that do not
+ *   overlap; A [n_tok x heads * width] bf16 out (o's input), or NULL to keep
+ *   it in ws.
  * ws: sgpt_attn_block_workspace_bytes bytes (0 = bad sizes). 1 <= n_tok <=
  * 2^30; heads * width <= 32768. */
 typedef struct sgpt_attn_block {

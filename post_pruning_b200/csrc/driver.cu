@@ -68,9 +68,9 @@ __global__ void swiglu_kernel(const float* __restrict__ G, const float* __restri
   }
 }
 
-// x' = bf16(x + d).
-__global__ void residual_kernel(const uint16_t* __restrict__ X, const float* __restrict__ D, long long count,
-                                uint16_t* __restrict__ Xn, const int* info) {
+// x' = bf16(x + d); x' may be written over x.
+__global__ void residual_kernel(const uint16_t* X, const float* __restrict__ D, long long count, uint16_t* Xn,
+                                const int* info) {
   if (info_set(info)) return;
   for (long long q = (long long)blockIdx.x * blockDim.x + threadIdx.x; q < count / 4;
        q += (long long)gridDim.x * blockDim.x) {
@@ -372,9 +372,10 @@ cudaError_t launch_prune_attn_block(const sgpt_attn_block& blk, int hidden, int 
     if ((e = prune_o()) != cudaSuccess) return e;
     return output();
   }
-  // parallel: the dense block's attention output and result first
+  // parallel: the dense block's attention output first; its result once q, k
+  // and v have been pruned from x, which x' may be written over (W_o is dense
+  // until the end)
   if ((e = mix()) != cudaSuccess) return e;
-  if ((e = output()) != cudaSuccess) return e;
   DriverStreams* ds = nullptr;
   std::lock_guard<std::mutex> lock(g_drv_mu);
   if ((e = driver_streams(&ds)) != cudaSuccess) return e;
@@ -388,6 +389,7 @@ cudaError_t launch_prune_attn_block(const sgpt_attn_block& blk, int hidden, int 
   const cudaError_t ej = es == cudaSuccess ? cudaStreamWaitEvent(st, ds->join, 0) : es;
   if (e != cudaSuccess) return e;
   if (ej != cudaSuccess) return ej;
+  if ((e = output()) != cudaSuccess) return e;
   return prune_o();
 }
 
