@@ -288,8 +288,9 @@ sgpt_status sgpt_prune_layer(float* W, int d_out, int d_in, int ldw, const uint1
  * blk: the three weight matrices (fp32, row-major, in: dense, out: pruned;
  *   W_gate, W_up [inter x hidden], W_down [hidden x inter]) and their masks
  *   ([inter x hidden/32], [hidden x inter/32]).
- * X_next [n_tok x hidden] bf16 out; Z [n_tok x inter] bf16 out (the down
- *   projection's input), or NULL to keep it in ws.
+ * X_next [n_tok x hidden] bf16 out, X itself or a buffer that does not
+ *   overlap it; Z [n_tok x inter] bf16 out (the down projection's input), or
+ *   NULL to keep it in ws.
  * p: pattern, block size, damping and qbits as for sgpt_prune (one grid per
  *   matrix from its dense weights); p->forced and p->qgrid must be 0/NULL.
  * ws: sgpt_mlp_block_workspace_bytes(hidden, inter, n_tok) bytes.

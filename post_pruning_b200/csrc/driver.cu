@@ -242,9 +242,10 @@ cudaError_t launch_prune_mlp_block(const sgpt_mlp_block& blk, int h, int f, cons
     // the next block's input from the pruned block
     return forward_down(blk, h, f, X, n, X_next, w, info, st);
   }
-  // parallel: record the dense block's down input and output first
+  // parallel: record the dense block's down input first; its output once gate
+  // and up have been pruned from x, which x' may be written over (W_down is
+  // dense until the end)
   if ((e = forward(blk, h, f, X, n, X_next, w, info, st)) != cudaSuccess) return e;
-  if ((e = forward_down(blk, h, f, X, n, X_next, w, info, st)) != cudaSuccess) return e;
   DriverStreams* ds = nullptr;
   std::lock_guard<std::mutex> lock(g_drv_mu);
   if ((e = driver_streams(&ds)) != cudaSuccess) return e;
@@ -261,6 +262,7 @@ cudaError_t launch_prune_mlp_block(const sgpt_mlp_block& blk, int h, int f, cons
   const cudaError_t ej = es == cudaSuccess ? cudaStreamWaitEvent(st, ds->join, 0) : es;
   if (e != cudaSuccess) return e;
   if (ej != cudaSuccess) return ej;
+  if ((e = forward_down(blk, h, f, X, n, X_next, w, info, st)) != cudaSuccess) return e;
   if ((e = launch_factor(w.H2, n, f, p.damp, w.U2, w.inner, info, st)) != cudaSuccess) return e;
   return prune_one(blk.W_down, h, f, w.U2, blk.mask_down, w.inner);
 }
