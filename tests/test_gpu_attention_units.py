@@ -15,6 +15,62 @@ from test_gpu_attention import DEV, _check, _inputs, _run
 pytestmark = pytest.mark.gpu
 
 
+# several hundred CTAs of several blocks each: units of two heads (an even group) and of two row tiles (an odd one),
+# one-tile and two-tile units of very different lengths in turn, ends inside a tile
+LENS = [900, 129, 700, 1, 640] * 4
+SHAPES = [(16, 2, 128), (16, 2, 64), (12, 12, 128), (12, 12, 64), (9, 3, 128), (9, 3, 64)]
+
+
+@pytest.mark.parametrize("heads,kv,width", SHAPES)
+def test_attention_several_units_per_cta(heads, kv, width):
+    """Values, and the same bits again after a launch on other inputs in
+    between: which CTA takes which unit differs from launch to launch."""
+    Q, K, V, off = _inputs(LENS, heads, kv, width)
+    want = _run(Q, K, V, off)
+    _check(want, Q, K, V, off)
+    other = _inputs(LENS[::-1], heads, kv, width, seed=9)
+    for _ in range(5):
+        _run(*other)
+        assert torch.equal(_run(Q, K, V, off), want)
+
+
+@pytest.mark.parametrize("heads,kv,width", SHAPES)
+def test_attention_several_units_of_rising_scores(heads, kv, width):
+    """The running maximum moves in most blocks, so results are rescaled while
+    the other tile's scores, or the next unit's, are under way; rows of one
+    buffer, and rows of NaN behind the last sequence."""
+    g = torch.Generator(device=DEV).manual_seed(heads)
+    n = sum(LENS)
+    buf = torch.randn(n + 40, (heads + 2 * kv) * width, device=DEV, generator=g)
+    buf[:n, heads * width:(heads + kv) * width] *= torch.cat([torch.linspace(0.05, 3.0, m) for m in LENS]).to(DEV)[:, None]
+    buf[n:] = float("nan")
+    Q, K, V = (t.unflatten(1, (-1, width)) for t in
+               buf.bfloat16().split([heads * width, kv * width, kv * width], 1))
+    off = torch.tensor([0] + LENS, device=DEV).cumsum(0).to(torch.int32)
+    O = _run(Q, K, V, off)
+    _check(O, Q, K, V, off)
+    assert bool((O[n:] == 7).all())
+
+
+@pytest.mark.parametrize("heads,kv,width", [(16, 2, 128), (9, 3, 64)])
+def test_attention_several_units_time_out(heads, kv, width):
+    """A wait that runs out in a launch whose CTAs take others' units."""
+    Q, K, V, off = _inputs(LENS, heads, kv, width)
+    want = _run(Q, K, V, off)
+    O = torch.empty_like(want)
+    info = pp.new_info()
+    pp.set_wait_limit(1)
+    try:
+        pp.attention(Q, K, V, off, O, info)
+        assert pp.sync_status(info) == 4                                  # TIMEOUT
+    finally:
+        pp.set_wait_limit(0)
+    pp.info_clear(info)
+    pp.attention(Q, K, V, off, O, info)
+    pp.raise_on_info(info)
+    assert torch.equal(O, want)
+
+
 @pytest.mark.parametrize("heads,kv,width", [(16, 4, 128), (8, 8, 64)])
 def test_attention_more_ctas_than_units(heads, kv, width):
     """The launch has a CTA for every unit that the lengths could give; here
