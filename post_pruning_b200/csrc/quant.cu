@@ -21,7 +21,8 @@
 // codes. A warp takes a row up to 1024 elements, a CTA of 128 to 1024 threads a
 // longer one, small enough that several rows are in flight per SM, with no
 // more registers than the row needs (16384 gated rows of 5120 with four
-// vectors of eight per thread: 90 us; with the three that they need: 72). Of
+// vectors of eight per thread: 92 us; with the three that they need: 75; 2048
+// rows of 16416 with 13 vectors: 21.1, with their nine 18.8). Of
 // 4096 rows on a warp takes up to 2048 elements too (gated: 1280): it has no
 // barrier to wait at (8192 rows of 1248 in a CTA each 10.2 us, in a warp 6.9;
 // 2048 rows 3.4 and 3.8). A few long rows (above 8192, n <= 64: decoding) are
@@ -421,8 +422,7 @@ cudaError_t launch(const uint16_t* X, const uint16_t* U, long long n, int d, lon
     if (vecs <= kGatedThreads * kGatedVec) return as(launch_gated<kGatedVec>);
     return as(launch_as<1024, 4, 1, true>);
   }
-  if (d <= 26624) return as(launch_as<256, 13, 1, false>);
-  return as(launch_as<256, 16, 1, false>);
+  return as(fit<256, 9, 16, false>(vecs));
 }
 
 }  // namespace
