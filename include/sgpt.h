@@ -372,8 +372,8 @@ sgpt_status sgpt_quant_codes(const float* W, int d_out, int d_in, int ldw, const
  * ties to even, and sums[t] = sum_k Xq[t][k]. The division is IEEE fp32; for
  * bf16 X the codes are the exact ones. A row of zeros has scale 0. A row with
  * a NaN or an infinity gets codes 0 and scale NaN and sets
- * SGPT_INFO_NONFINITE (the other rows are then unspecified). 0 <= n <= 2^30; n == 0 launches nothing. Inputs and outputs must not
- * overlap. */
+ * SGPT_INFO_NONFINITE (the other rows are then unspecified). 0 <= n <= 2^30;
+ * n == 0 launches nothing. Inputs and outputs must not overlap. */
 sgpt_status sgpt_quant_tokens(const uint16_t* X, int64_t n, int d, int64_t ldx, int8_t* Xq, float* scale,
                               int32_t* sums, int* dev_info, void* stream);
 
@@ -409,15 +409,18 @@ sgpt_status sgpt_linear_i8(const int8_t* Xq, const float* scale, const int32_t* 
  *     sequence are not written. Offsets that decrease or leave [0, n_tok] set
  *     SGPT_INFO_BAD_LENGTHS (the output is then unspecified).
  *   width 64 or 128 (else SGPT_ERR_UNSUPPORTED), heads a multiple of
- *     kv_heads, scale > 0 (usually width^-1/2), 0 <= n_tok, n_seq <= 2^30.
+ *     kv_heads and at most 65536, scale > 0 (usually width^-1/2), 0 <= n_tok,
+ *     n_seq <= 2^30.
  * Scores, softmax and sums in fp32; the softmax's weights enter the second
  * product in bf16; O is rounded once. Values in masked places (later rows,
  * other sequences, rows outside) never reach a row's result as long as the
  * row's own sequence is finite; a result that is not finite sets
- * SGPT_INFO_NONFINITE. O must not overlap Q, K or V. The same call gives the
- * same bits; n_tok, n_seq and the head counts decide whether the sums of a
- * row are formed in one or in several parts, so the same sequence packed with
- * others may differ in its last rounding. */
+ * SGPT_INFO_NONFINITE (rows of other sequences are then right or left as they
+ * were: what runs later in the same call sees the error). O must not overlap
+ * Q, K or V. The same call gives the same bits; n_tok, n_seq and the head
+ * counts decide whether the sums of a row are formed in one or in several
+ * parts, so the same sequence packed with others may differ in its last
+ * rounding. */
 sgpt_status sgpt_attention(const uint16_t* Q, int64_t ldq, const uint16_t* K, int64_t ldk, const uint16_t* V,
                            int64_t ldv, const int32_t* offsets, int n_seq, int64_t n_tok, int heads, int kv_heads,
                            int width, float scale, uint16_t* O, int64_t ldo, int* dev_info, void* stream);

@@ -52,7 +52,10 @@ constexpr int kThreads = 384;                   // 2 x 4 softmax warps, TMA, MMA
 // registers a thread after the split: 2 x 200 + 104 = 3 x 168, what the block is launched with
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr int kBox = kT * 128;                  // 16 KB: 128 rows x 64 bf16
-constexpr int kFree = 8;                        // barriers that free ring slots, more than ring slots
+// Barriers that free ring slots, one for each group of slots that is freed
+// together: at most kStages groups are outstanding (each holds a slot), so with
+// as many barriers a wait is never more than one phase behind.
+constexpr int kFree = 8;
 constexpr float kGrow = 8.f;                    // exponent growth that moves the running maximum
 
 __host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBox; }
@@ -196,7 +199,7 @@ struct Search {
 // first: f(u) units have the number u or a later one in their sequence, and
 // the search halves the interval of u. (One sequence after the other left the
 // long units of the last one to the end: ten prompts of 2 to 1355 rows took
-// 39 us instead of 27, 8 x 2048 rows 620 instead of 590.) A sequence's offsets
+// 39 us instead of 27, 8 x 2048 rows a twentieth longer.) A sequence's offsets
 // are used only if they lie inside the packed rows.
 __device__ Work find_work(const Shape& sh, const int32_t* cu, int index, int lane, Search& at_seq) {
   const int head_units = sh.pair ? sh.heads / 2 : sh.heads;
@@ -262,9 +265,10 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* v, bool wid
 // lane x has the pieces 0..3 of row x; out, lane x has piece x of the rows
 // 0..3. A store then writes 128 consecutive bytes of eight rows instead of 32
 // bytes of each of 32 rows, a quarter of the lines. For a width of 128 those
-// lines took 1900 of the epilogue's 2700 cycles (8 x 2048 rows, 64 heads on 8:
-// 526 -> 517 us at full clocks). It costs more than it saves for a width of 64 (half the
-// lines) and in units of one or two blocks, whose epilogue nothing hides.
+// lines took 1900 of the epilogue's 2700 cycles (8 x 2048 rows in a row, 64
+// heads on 8: 632 -> 616 us; 16 on 2: 157.6 -> 155.5; eight ragged prompts, 32
+// on 32: 144.5 -> 147.3). It costs more than it saves for a width of 64 (half
+// the lines) and in units of one or two blocks, whose epilogue nothing hides.
 __device__ __forceinline__ void quad_transpose(uint32_t (&v)[32], int lane) {
 #pragma unroll
   for (int bit = 1; bit < 4; bit <<= 1) {

@@ -30,10 +30,11 @@
 // operands, two accumulators so that one is drained under the other's MMAs.
 // A single CTA on 128 x 256 tiles is bound by shared memory (48 KB written and
 // 48 KB read per 512 cycles of MMA, above its 128 bytes per cycle): 2,890
-// TOP/s on 16384 x 5120 x 25600; the pair needs 32 + 32 KB: 3,420, its tensor
-// cores busy for 91 % of the time at the clock that the power allows. K in two
-// parts where there are few tiles. Tiles are walked in groups of 8 tile rows (rows fastest)
-// so that resident pairs share panels in L2.
+// TOP/s on 16384 x 5120 x 25600 as a single launch; the pair needs 32 + 32 KB:
+// 3,420, its tensor cores busy for 91 % of the time. In a row the power limit
+// leaves the pair 2,870 to 3,100. K in two parts where there are few tiles.
+// Tiles are walked in groups of 8 tile rows (rows fastest) so that resident
+// pairs share panels in L2.
 //
 // linear_i8_split_kernel, few tiles: one tile of 128 channels x 16..64 tokens
 // per CTA, or per cluster of CTAs that split K and add their int32 accumulators

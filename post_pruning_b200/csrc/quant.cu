@@ -22,7 +22,7 @@
 // longer one, small enough that several rows are in flight per SM, with no
 // more registers than the row needs (16384 gated rows of 5120 with four
 // vectors of eight per thread: 92 us; with the three that they need: 75; 2048
-// rows of 16416 with 13 vectors: 21.1, with their nine 18.8). Of
+// rows of 16416 with 13 vectors: 21.1, with their nine 19.2). Of
 // 4096 rows on a warp takes up to 2048 elements too (gated: 1280): it has no
 // barrier to wait at (8192 rows of 1248 in a CTA each 10.2 us, in a warp 6.9;
 // 2048 rows 3.4 and 3.8). A few long rows (above 8192, n <= 64: decoding) are
