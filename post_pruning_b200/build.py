@@ -70,6 +70,8 @@ def _build_marshal() -> None:
         with open(stamp) as f:
             if f.read() == torch.__version__:
                 return
+    if os.path.exists(MARSHAL):         # if it cannot be compiled again, none is better than one of other sources
+        os.remove(MARSHAL)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",

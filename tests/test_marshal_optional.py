@@ -51,6 +51,8 @@ def test_module_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
 
     def run(cmd, **kw):
         ran.append(cmd)
+        assert not module.exists()                         # nothing of other sources stays if this fails
+        module.touch()
         return subprocess.CompletedProcess(cmd, 0, "", "")
 
     module = tmp_path / "_marshal.so"
